@@ -245,6 +245,8 @@ const char* rq_status_str(int status) {
     case RQ_ERR_ALIAS: return "output overlaps an input";
     case RQ_ERR_SCRATCH: return "needs more than the static scratch of rq_gemm_small_m_noalloc";
     case RQ_ERR_DEGENERATE: return "every weight is equal: no gap to normalise";
+    case RQ_ERR_WORKSPACE: return "the call needs a larger workspace";
+    case RQ_ERR_VALUE: return "scalar argument outside its range";
   }
   return "unknown status";
 }

@@ -25,6 +25,8 @@ RQ_ERR_HIP = -7
 RQ_ERR_ALIAS = -8
 RQ_ERR_SCRATCH = -9
 RQ_ERR_DEGENERATE = -10
+RQ_ERR_WORKSPACE = -11
+RQ_ERR_VALUE = -12
 RQ_PROXY_MAX_K = 16
 
 RQ_W8_SYM = 1
@@ -44,7 +46,8 @@ EXPORTS = (
     "rq_gemv_w8g64", "rq_gemv_w4sb256", "rq_gemv_f16", "rq_gemm_small_m", "rq_fused_rkv",
     "rq_quantize_act", "rq_gemm_fp8", "rq_gemm_int8", "rq_gemm_int8_acc", "rq_host_convert",
     "rq_gemm_w4", "rq_quantize_aw", "rq_workspace_bytes", "rq_gemm_small_m_noalloc", "rq_stream_read",
-    "rq_proxy", "rq_plan_small_m",
+    "rq_proxy", "rq_plan_small_m", "rq_time_mix", "rq_time_mix_backward", "rq_time_mix_backward_bytes",
+    "rq_shift_norm", "rq_shift_norm_backward", "rq_head_gate", "rq_head_gate_backward",
 )
 
 # rq_plan.kernel
@@ -80,7 +83,7 @@ def lib():
         if not os.path.exists(_LIB_PATH):
             raise RuntimeError("librq.so is not built (run gemm_rwkv_amd.build or __graft_entry__.build())")
         L = ctypes.CDLL(_LIB_PATH)
-        vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        vp, i64, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
         qp = ctypes.POINTER(_QW)
         sig = {
             "rq_abi_version": ([], i32),
@@ -101,6 +104,15 @@ def lib():
             "rq_proxy": ([vp, i64, i32, vp, vp, vp, vp], i32),
             "rq_host_convert": ([i32, vp, vp, i64], i32),
             "rq_plan_small_m": ([qp, i64, i64, sz, ctypes.POINTER(_Plan)], i32),
+            "rq_time_mix": ([i32] + [vp] * 6 + [i64] * 3 + [vp, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp], i32),
+            "rq_time_mix_backward": ([i32] + [vp] * 6 + [i64] * 3 + [vp, i64] + [vp] * 11 + [sz, vp], i32),
+            "rq_time_mix_backward_bytes": ([i64] * 3, sz),
+            "rq_shift_norm": ([i32, vp, vp, f32, i64, i64, i64, vp, i64, vp, vp, f32, vp, i64, vp, vp, vp, i64, vp, vp,
+                               i64, vp], i32),
+            "rq_shift_norm_backward": ([i32, vp, f32, i64, i64, i64, vp, i64, vp, vp, f32, vp, i64, vp, vp, i64] +
+                                       [vp] * 9 + [sz, vp], i32),
+            "rq_head_gate": ([i32] + [vp] * 5 + [i64] * 3 + [vp, vp, f32, vp, vp, i64, vp], i32),
+            "rq_head_gate_backward": ([i32] + [vp] * 5 + [i64] * 3 + [vp, vp, f32] + [vp] * 11 + [sz, vp], i32),
         }
         for name in ("rq_gemv_w4g16", "rq_gemv_w4g32", "rq_gemv_w4g64", "rq_gemv_w8g16",
                      "rq_gemv_w8g32", "rq_gemv_w8g64", "rq_gemv_w4sb256", "rq_gemv_f16"):
@@ -363,6 +375,89 @@ def rq_gemm_int8_acc(xq, m, w, acc, stream=None, ws=None):
     st = lib().rq_gemm_int8_acc(_ptr(xq), m, ctypes.byref(d), _ptr(acc), *_ws(ws), _stream(stream))
     _check(st, "rq_gemm_int8_acc")
     return acc
+
+
+# --------------------------------------------------------------------------
+# time mixing: the operators between a layer's projections
+# --------------------------------------------------------------------------
+
+
+def _fresh_ws(ws, nbytes, stream):
+    """(pointer, bytes, tensor) of a workspace that must hold nbytes: the
+    caller's, or, for None, memory of torch's allocator for this call."""
+    if ws is not None or not torch.cuda.is_available():
+        return _ws(False if ws is None else ws) + (None,)
+    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        t.record_stream(stream)
+    return t.data_ptr(), nbytes, t
+
+
+def rq_time_mix(dtype, r, w, k, v, a, b, tokens, heads, ld, cu, nseq, state_in, state_out, slots, nslots, y, ldy,
+                stream=None, ws=None):
+    """The state recurrence S_t = S_{t-1} diag(w_t) + (S_{t-1} a_t) b_t^T + v_t k_t^T, y_t = S_t r_t per head of 64.
+    dtype: RQ_F16 or RQ_BF16; cu, states and slots may be None."""
+    st = lib().rq_time_mix(dtype, _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(a), _ptr(b), tokens, heads, ld, _ptr(cu), nseq,
+                           _ptr(state_in), _ptr(state_out), _ptr(slots), nslots, _ptr(y), ldy, *_ws(ws), _stream(stream))
+    _check(st, "rq_time_mix")
+    return y
+
+
+def rq_time_mix_backward_bytes(tokens, heads, nseq):
+    return int(lib().rq_time_mix_backward_bytes(tokens, heads, nseq))
+
+
+def rq_time_mix_backward(dtype, r, w, k, v, a, b, tokens, heads, ld, cu, nseq, state_in, dy, dstate_out, dr, dw, dk, dv, da,
+                         db, dstate_in, stream=None, ws=None):
+    """Gradients of rq_time_mix.  ws None: memory of torch's allocator for this
+    call, of rq_time_mix_backward_bytes()."""
+    p, n, keep = _fresh_ws(ws, lib().rq_time_mix_backward_bytes(tokens, heads, nseq), stream)
+    st = lib().rq_time_mix_backward(dtype, _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(a), _ptr(b), tokens, heads, ld, _ptr(cu),
+                                    nseq, _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dr), _ptr(dw), _ptr(dk),
+                                    _ptr(dv), _ptr(da), _ptr(db), _ptr(dstate_in), p, n, _stream(stream))
+    _check(st, "rq_time_mix_backward")
+    return dr, dw, dk, dv, da, db
+
+
+def rq_shift_norm(dtype, x, delta, alpha, tokens, width, ld, cu, nseq, gamma, beta, eps, mu, nmix, shift_in, shift_out,
+                  slots, nslots, x_out, out, ldo, stream=None):
+    """x' = x + alpha delta, layer norm h, and nmix mixtures h + (h of the token before - h) mu_i."""
+    st = lib().rq_shift_norm(dtype, _ptr(x), _ptr(delta), alpha, tokens, width, ld, _ptr(cu), nseq, _ptr(gamma), _ptr(beta),
+                             eps, _ptr(mu), nmix, _ptr(shift_in), _ptr(shift_out), _ptr(slots), nslots, _ptr(x_out),
+                             _ptr(out), ldo, _stream(stream))
+    _check(st, "rq_shift_norm")
+    return out
+
+
+def rq_shift_norm_backward(dtype, x, alpha, tokens, width, ld, cu, nseq, gamma, beta, eps, mu, nmix, shift_in, dout, ldo,
+                           dx_out, dshift_out, dx, ddelta, dshift_in, dgamma, dbeta, dmu, stream=None, ws=None):
+    """Gradients of rq_shift_norm at x' = x."""
+    st = lib().rq_shift_norm_backward(dtype, _ptr(x), alpha, tokens, width, ld, _ptr(cu), nseq, _ptr(gamma), _ptr(beta), eps,
+                                      _ptr(mu), nmix, _ptr(shift_in), _ptr(dout), ldo, _ptr(dx_out), _ptr(dshift_out),
+                                      _ptr(dx), _ptr(ddelta), _ptr(dshift_in), _ptr(dgamma), _ptr(dbeta), _ptr(dmu),
+                                      *_ws(ws), _stream(stream))
+    _check(st, "rq_shift_norm_backward")
+    return dx
+
+
+def rq_head_gate(dtype, y, r, k, v, g, tokens, heads, ld, gamma, beta, eps, u, out, ldo, stream=None):
+    """(norm of each head of y * gamma + beta + (sum r k u) v) * g."""
+    st = lib().rq_head_gate(dtype, _ptr(y), _ptr(r), _ptr(k), _ptr(v), _ptr(g), tokens, heads, ld, _ptr(gamma), _ptr(beta),
+                            eps, _ptr(u), _ptr(out), ldo, _stream(stream))
+    _check(st, "rq_head_gate")
+    return out
+
+
+def rq_head_gate_backward(dtype, y, r, k, v, g, tokens, heads, ld, gamma, beta, eps, u, dout, dy, dr, dk, dv, dg, dgamma,
+                          dbeta, du, stream=None, ws=None):
+    """Gradients of rq_head_gate."""
+    st = lib().rq_head_gate_backward(dtype, _ptr(y), _ptr(r), _ptr(k), _ptr(v), _ptr(g), tokens, heads, ld, _ptr(gamma),
+                                     _ptr(beta), eps, _ptr(u), _ptr(dout), _ptr(dy), _ptr(dr), _ptr(dk), _ptr(dv),
+                                     _ptr(dg), _ptr(dgamma), _ptr(dbeta), _ptr(du), *_ws(ws), _stream(stream))
+    _check(st, "rq_head_gate_backward")
+    return dy
 
 
 def rq_stream_read(buf, nbytes, sink, stream=None):

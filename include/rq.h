@@ -83,7 +83,9 @@ enum rq_status {
   RQ_ERR_HIP = -7,       /* a HIP runtime call failed                          */
   RQ_ERR_ALIAS = -8,     /* an output overlaps an input                        */
   RQ_ERR_SCRATCH = -9,   /* too large for rq_gemm_small_m_noalloc's scratch    */
-  RQ_ERR_DEGENERATE = -10 /* rq_proxy: every weight equal (no gap to normalise) */
+  RQ_ERR_DEGENERATE = -10, /* rq_proxy: every weight equal (no gap to normalise) */
+  RQ_ERR_WORKSPACE = -11, /* the call needs a larger workspace                 */
+  RQ_ERR_VALUE = -12      /* a scalar argument outside its range               */
 };
 
 /*
@@ -375,6 +377,117 @@ int rq_gemm_int8(const int8_t *xq, const float *sx, int64_t m, const rq_qweight 
  * for bit-exact checking of the integer contraction. */
 int rq_gemm_int8_acc(const int8_t *xq, int64_t m, const rq_qweight *w, int32_t *acc,
                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Time mixing: the operators between a layer's projections.
+ *
+ * rq_shift_norm, the projections, rq_time_mix, rq_head_gate and the output
+ * projection together are RWKV-7's time mixing; rq_shift_norm with one mixture
+ * also opens the channel mixing.  Each has its gradient.  The pages describe
+ * no such operator; the mathematics is written out at each entry.
+ *
+ * Types.  `dtype` is the type of every activation and of its gradients: RQ_F16
+ * or RQ_BF16 (RQ_ERR_FORMAT otherwise), rounded to nearest even once, when it
+ * is stored.  Parameters, their gradients and the recurrence's states are
+ * fp32; every sum, statistic and state is held in fp32 or more.
+ *
+ * Rows.  An activation is [tokens][ld] with ld >= the width and ld % 8 == 0
+ * (RQ_ERR_ALIGN), tokens counted over all sequences.
+ *
+ * Sequences.  The rows of nseq sequences follow one another.  cu (device,
+ * int32, 4-byte aligned) holds their nseq + 1 offsets, cu[0] = 0,
+ * cu[nseq] = tokens, not falling; a sequence may be empty, and its state is
+ * carried over.  Offsets that break this rule are clamped to 0..tokens (no
+ * access leaves the arrays, the outputs are unspecified).  cu == NULL: nseq
+ * sequences of tokens / nseq rows each (RQ_ERR_SHAPE if that does not divide).
+ *
+ * Slots.  What a sequence carries from call to call lies in an array of nslots
+ * entries; sequence i uses entry slots[i] (device, int32 [nseq], 4-byte
+ * aligned), or entry i with slots == NULL (then nslots >= nseq).  A sequence
+ * whose slot lies outside 0..nslots-1 starts from zeros and leaves nothing
+ * behind.  Two sequences of one call must not share an entry.  The array
+ * written may be the array read (in place) or disjoint from it.  A NULL input
+ * array means zeros, a NULL output array that nothing is kept.
+ *
+ * Workspaces are as for the products; the split counters at their head are
+ * neither read nor written.  None of these calls allocates or synchronizes,
+ * and each gives the same bits for the same arguments.  nseq * heads and nseq
+ * stay below 2^23, tokens * ld below 2^40.
+ */
+
+/* The state recurrence, per head of 64 channels with a state S[64][64] (rows:
+ * channels of v; columns: channels of k):
+ *     w_t = exp(-exp(-1/2) * sigmoid(w[t]))          (in 0.545..1)
+ *     S_t = S_{t-1} diag(w_t) + (S_{t-1} a_t) b_t^T + v_t k_t^T
+ *     y_t = S_t r_t
+ * RWKV-7 has a = -kappa and b = kappa * rate with a unit vector kappa.
+ * r, w, k, v, a, b: [tokens][ld]; y: [tokens][ldy]; states: fp32
+ * [nslots][heads][64][64].  The workspace only makes long sequences faster: a
+ * call that has too few sequences and heads to fill the GPU cuts them into
+ * segments when it holds the segments' states. */
+int rq_time_mix(int dtype, const void *r, const void *w, const void *k, const void *v, const void *a, const void *b,
+                int64_t tokens, int64_t heads, int64_t ld, const int32_t *cu, int64_t nseq, const float *state_in,
+                float *state_out, const int32_t *slots, int64_t nslots, void *y, int64_t ldy, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/* Its gradient: from dy [tokens][ld] and dstate_out (fp32 [nseq][heads][64][64],
+ * NULL: zeros) the gradients of the six inputs (dw that of the raw decay) and
+ * of the state, dstate_in (may be NULL).  state_in is the forward call's,
+ * [nseq][heads][64][64] without slots (NULL: zeros).  The workspace holds the
+ * states along the sequences: at least rq_time_mix_backward_bytes(tokens,
+ * heads, nseq) bytes (host-only; 0 for arguments out of range), else
+ * RQ_ERR_WORKSPACE. */
+size_t rq_time_mix_backward_bytes(int64_t tokens, int64_t heads, int64_t nseq);
+int rq_time_mix_backward(int dtype, const void *r, const void *w, const void *k, const void *v, const void *a,
+                         const void *b, int64_t tokens, int64_t heads, int64_t ld, const int32_t *cu, int64_t nseq,
+                         const float *state_in, const void *dy, const float *dstate_out, void *dr, void *dw, void *dk,
+                         void *dv, void *da, void *db, float *dstate_in, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* Residual, layer norm and the mixtures with the token before:
+ *     x'_t = x_t + alpha delta_t            (delta NULL: x' = x)
+ *     h_t = (x'_t - mean) / sqrt(var + eps) * gamma + beta
+ *     out_i,t = h_t + (h_{t-1} - h_t) * mu_i,   i = 0..nmix-1, 1 <= nmix <= 8
+ * h before a sequence's first row is its entry of shift_in, and its last h
+ * goes to shift_out; both [nslots][width] of dtype.  x, delta, x_out (may be
+ * NULL): [tokens][ld]; out: nmix planes [tokens][ldo], one after the other;
+ * gamma, beta: [width]; mu: [nmix][width].  h and the sum x' are not rounded
+ * before their use.  width: a multiple of 8 (RQ_ERR_ALIGN), at most 8192;
+ * eps >= 0 (RQ_ERR_VALUE). */
+int rq_shift_norm(int dtype, const void *x, const void *delta, float alpha, int64_t tokens, int64_t width, int64_t ld,
+                  const int32_t *cu, int64_t nseq, const float *gamma, const float *beta, float eps, const float *mu,
+                  int64_t nmix, const void *shift_in, void *shift_out, const int32_t *slots, int64_t nslots,
+                  void *x_out, void *out, int64_t ldo, void *stream);
+
+/* Its gradient at x' = x: from dout (planes as out), dx_out ([tokens][ld], the
+ * gradient that reaches x' elsewhere; NULL: zeros) and dshift_out ([nseq][width];
+ * NULL: zeros) to dx, ddelta = alpha dx (may be NULL), dshift_in ([nseq][width],
+ * may be NULL), dgamma, dbeta and dmu, all written, not accumulated.  shift_in
+ * is [nseq][width] without slots.  The workspace holds partial sums of the
+ * parameters' gradients; without one a single workgroup walks all rows. */
+int rq_shift_norm_backward(int dtype, const void *x, float alpha, int64_t tokens, int64_t width, int64_t ld,
+                           const int32_t *cu, int64_t nseq, const float *gamma, const float *beta, float eps,
+                           const float *mu, int64_t nmix, const void *shift_in, const void *dout, int64_t ldo,
+                           const void *dx_out, const void *dshift_out, void *dx, void *ddelta, void *dshift_in,
+                           float *dgamma, float *dbeta, float *dmu, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* The norm of each head's 64 outputs, the bonus and the gate:
+ *     out = ((y - mean) / sqrt(var + eps) * gamma + beta + (sum_j r_j k_j u_j) v) * g
+ * with mean, var and the sum over a head's channels.  y, r, k, v, g:
+ * [tokens][ld]; out: [tokens][ldo]; gamma, beta, u: [64 heads].  RWKV-7 has
+ * eps = 64e-5. */
+int rq_head_gate(int dtype, const void *y, const void *r, const void *k, const void *v, const void *g, int64_t tokens,
+                 int64_t heads, int64_t ld, const float *gamma, const float *beta, float eps, const float *u, void *out,
+                 int64_t ldo, void *stream);
+
+/* Its gradient: dout and the five row gradients are [tokens][ld].  Workspace
+ * as for rq_shift_norm_backward. */
+int rq_head_gate_backward(int dtype, const void *y, const void *r, const void *k, const void *v, const void *g,
+                          int64_t tokens, int64_t heads, int64_t ld, const float *gamma, const float *beta, float eps,
+                          const float *u, const void *dout, void *dy, void *dr, void *dk, void *dv, void *dg,
+                          float *dgamma, float *dbeta, float *du, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 /* Measurement aid: reads `bytes` of device memory at buf (16-byte aligned,
  * bytes % 16 == 0) with 16-byte non-temporal loads spread over every compute
