@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t kMostWidth = 8192;  // a row is held in the registers of one workgroup
 constexpr int64_t kMostMix = 8;
-constexpr int64_t kMostGrid = (int64_t)1 << 23;  // workgroups of one launch
+constexpr int64_t kMostGrid = (int64_t)1 << 22;  // workgroups of one launch
 
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 

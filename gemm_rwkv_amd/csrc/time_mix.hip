@@ -10,6 +10,7 @@
 // sums S a and S r are four lane rotations.  A run of up to sixteen tokens is
 // staged in LDS as fp32.
 #include "mix.h"
+#include "time_mix_chunk.h"
 
 namespace rq {
 
@@ -89,8 +90,87 @@ __global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p) {
     for (int j = 0; j < 4; ++j) *(float4*)(p.state_out + state + (row + 4 * j) * kHead + col) = S[j];
 }
 
+// chunk kernel: one workgroup of eight waves per (sequence, head).  Waves 0-3
+// hold the state, sixteen channels of v each, and take it from chunk to chunk;
+// waves 4-7 prepare the chunks' operands, every fourth chunk each, in four
+// steps that they take one behind the other.  A barrier ends each step, in
+// which one chunk is finished and the one before it used: chunk c is written
+// in steps c + 2 and c + 3 into one of three LDS buffers and read in step
+// c + 4.  All eight waves pass chunks + 4 barriers.
+namespace {
+constexpr int kBuffers = 3;
+constexpr int kPreps = 4;
+}  // namespace
+
+template <typename T>
+__global__ void __launch_bounds__(512) time_mix_chunk_kernel(TimeMix p) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  ChunkOps* ops = (ChunkOps*)lds;
+  const int head = blockIdx.x % p.heads, s = blockIdx.x / p.heads;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int begin, end;
+  seq_span(p.seq, s, begin, end);
+  const int chunks = (end - begin + kChunk - 1) / kChunk;
+  if (wave >= 4) {
+    const int mine = wave - 4;
+    int steps = chunks + kPreps;
+    ChunkPrep<T> prep;
+    if (mine < chunks) prep.load(p, head, begin + mine * kChunk, min(kChunk, end - begin - mine * kChunk), lane);
+    for (int i = 0; i < mine && steps > 0; ++i, --steps) __syncthreads();
+    for (int c = mine; c < chunks; c += kPreps) {
+      ChunkOps& o = ops[c % kBuffers];
+      prep.decays();
+      __syncthreads();
+      prep.factors();
+      __syncthreads();
+      prep.put_rows(o, lane);
+      if (c + kPreps < chunks) {
+        const int t = (c + kPreps) * kChunk;
+        prep.load(p, head, begin + t, min(kChunk, end - begin - t), lane);
+      }
+      prep.grams();
+      __syncthreads();
+      prep.solve(o, lane);
+      __syncthreads();
+      steps -= kPreps;
+    }
+    for (; steps > 0; --steps) __syncthreads();
+    return;
+  }
+  const int slot = slot_of(p.slots, s);
+  const size_t state = ((size_t)(slot < 0 ? 0 : slot) * p.heads + head) * kHead * kHead;
+  ChunkState<T> st;
+  st.load(p.state_in && slot >= 0 ? p.state_in + state : nullptr, wave, lane);
+  for (int i = 0; i < kPreps; ++i) __syncthreads();
+  const int q = lane & 15, g = lane >> 4;
+  for (int c = 0; c < chunks; ++c) {
+    const float4v y = st.step(ops[c % kBuffers], wave, lane);
+    const int t = begin + c * kChunk + 4 * g;
+    uint16_t* to = (uint16_t*)p.y + (size_t)t * p.ldy + head * kHead + 16 * wave + q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i < end) to[(size_t)i * p.ldy] = (uint16_t)T::down2(y[i], 0.f);
+    __syncthreads();
+  }
+  if (p.state_out && slot >= 0) st.store(p.state_out + state, wave, lane);
+}
+
+namespace {
+template <typename T>
+hipError_t start_chunks(const TimeMix& p, hipStream_t st) {
+  constexpr int kLds = kBuffers * sizeof(ChunkOps);
+  static const hipError_t attr = hipFuncSetAttribute((const void*)time_mix_chunk_kernel<T>,
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3((unsigned)p.seq.nseq * p.heads), dim3(512), kLds, st, p);
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_time_mix(const TimeMix& p, bool bf16, hipStream_t st) {
   const dim3 grid((unsigned)p.seq.nseq * p.heads), block(256);
+  if (p.seq.tokens > p.seq.nseq) return bf16 ? start_chunks<BF16>(p, st) : start_chunks<F16>(p, st);
   if (bf16)
     hipLaunchKernelGGL(time_mix_step_kernel<BF16>, grid, block, 0, st, p);
   else

@@ -1,0 +1,425 @@
+// The state recurrence in chunks of 16 tokens, on matrix instructions.
+//
+// With the decays accumulated from the chunk's start, L_t = sum_{s<=t} log w_s,
+//   A_t = a_t exp(L_{t-1}),  R_t = r_t exp(L_t),  B_t = b_t exp(-L_t),
+//   K_t = k_t exp(-L_t),     u_t = S_{t-1} a_t
+// the chunk is five products around the state S before it:
+//   U = T (A S^T + Ak V),              T = (1 - Ab)^-1
+//   Y = R S^T + Qb U + Qk V
+//   S' = (S + U^T B + V^T K) diag(exp L_15)
+// with Ab, Ak the strictly lower parts of A B^T, A K^T and Qb, Qk the lower
+// parts of R B^T, R K^T (16 x 16).  A decay is at least 0.545, so exp(-L) stays
+// below 1.7e4 and every factor is far inside fp32's and bf16's exponents.
+//
+// Precision.  A matrix instruction multiplies bf16 exactly and adds in fp32,
+// so an fp32 factor is cut into three bf16 terms that hold its 24 bits
+// exactly, and a product of two such factors keeps the six term products
+// above 2^-24 of it: what feeds the state is as exact as fp32.  Y, which is
+// rounded to 16 bits, takes two terms and three products (2^-16).
+//
+// Lanes.  l = 16 g + q.  A 16x16 result has row 4 g + i in register i and
+// column q.  As the B operand of the next product, its registers are the
+// slots of contraction index 4 g + i: the A operand only has to name its
+// slots alike, so the whole chain from state to state moves nothing between
+// lanes.  The state is held as S^T in four tiles; register i of tile n is
+// channel k = 32 (n / 2) + 8 g + 4 (n % 2) + i, so that the two tiles of an
+// operand hold eight consecutive channels.
+#pragma once
+
+#include "mix.h"
+
+namespace rq {
+
+typedef short short4v __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 16;
+
+__device__ __forceinline__ float4v mfma32(uint4 a, uint4 b, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ float4v mfma16(uint2 a, uint2 b, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, a), __builtin_bit_cast(short4v, b), c, 0, 0, 0);
+}
+
+// the upper halves of two words: a bf16 pair, cut (not rounded)
+__device__ __forceinline__ uint32_t high2(float lo, float hi) {
+  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+}
+__device__ __forceinline__ float cut(float x) {
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xffff0000u);
+}
+
+// Two fp32 values as NT bf16 pairs that add up to them: exactly for NT = 3
+// (8 bits each), within 2^-17 for NT = 2 (the last term is rounded).
+template <int NT>
+__device__ __forceinline__ void split2(float x, float y, uint32_t* t) {
+  t[0] = high2(x, y);
+  x -= cut(x);
+  y -= cut(y);
+  if (NT == 2) {
+    t[1] = BF16::down2(x, y);
+    return;
+  }
+  t[1] = high2(x, y);
+  x -= cut(x);
+  y -= cut(y);
+  t[2] = high2(x, y);
+}
+
+// Eight values as NT operands.
+template <int NT>
+__device__ __forceinline__ void split8(const float* x, uint4* t) {
+  uint32_t w[4][NT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2<NT>(x[2 * i], x[2 * i + 1], w[i]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) t[n] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+}
+// Four values of a 16x16 result as NT half operands.
+template <int NT>
+__device__ __forceinline__ void split4(float4v x, uint2* t) {
+  uint32_t w[2][NT];
+  split2<NT>(x[0], x[1], w[0]);
+  split2<NT>(x[2], x[3], w[1]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) t[n] = make_uint2(w[0][n], w[1][n]);
+}
+
+// The term products that count, smallest first: of three terms the six above
+// 2^-24, of two the three above 2^-16.
+template <int NT>
+__device__ __forceinline__ float4v mul32(const uint4* a, const uint4* b, float4v c) {
+  if (NT == 3) {
+    c = mfma32(a[0], b[2], c);
+    c = mfma32(a[2], b[0], c);
+    c = mfma32(a[1], b[1], c);
+  }
+  c = mfma32(a[0], b[1], c);
+  c = mfma32(a[1], b[0], c);
+  return mfma32(a[0], b[0], c);
+}
+template <int NT>
+__device__ __forceinline__ float4v mul16(const uint2* a, const uint2* b, float4v c) {
+  if (NT == 3) {
+    c = mfma16(a[0], b[2], c);
+    c = mfma16(a[2], b[0], c);
+    c = mfma16(a[1], b[1], c);
+  }
+  c = mfma16(a[0], b[1], c);
+  c = mfma16(a[1], b[0], c);
+  return mfma16(a[0], b[0], c);
+}
+
+// One chunk's operands in LDS, prepared by one wave and read by those that
+// hold the state.
+struct ChunkOps {
+  uint4 a[3][2][64];    // A: terms, channel halves, lanes (row q, channels 32 h + 8 g + j)
+  uint4 r[2][2][64];    // R, two terms
+  uint4 q[2][64];       // row q, slots j < 4: Qb at 4 g + j, j >= 4: Qk
+  uint2 t[3][64];       // T: row q, slots 4 g + i
+  uint2 ak[3][64];      // Ak: row q, slots 4 g + i
+  uint4 b[3][16 * 8];   // B rows [16][64 channels] in blocks of eight, see row_block
+  uint4 k[3][16 * 8];
+  uint4 v[2][16 * 8];   // V rows, two bf16 terms (one for bf16 rows)
+  float end[64];        // exp L_15 by channel
+};
+
+// Block c (eight channels) of row t.  A transposing read takes four rows and
+// two of every four channels of half a row at once; turning the halves of
+// rows 2 and 3 of each four puts all of them on different banks.
+__device__ __forceinline__ int row_block(int t, int c) { return t * 8 + (c ^ ((t & 2) << 1)); }
+
+// Four rows 4 g + 0..3 of one channel per lane, as half an operand: within
+// the 16 lanes of g, lane q fetches row 4 g + q / 4, four channels from ch(q % 4).
+__device__ __forceinline__ uint2 rows4(const uint4* rows, int g, int q, int channel) {
+  const int t = 4 * g + (q >> 2);
+  const uint2* p = (const uint2*)(rows + row_block(t, channel >> 3)) + ((channel >> 2) & 1);
+  typedef __attribute__((address_space(3))) short4v lds4;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p));
+}
+
+// One 16-byte block of row t, or zeros past the sequence's end.
+__device__ __forceinline__ uint4 block_or_zero(const void* base, size_t elem, bool held) {
+  return held ? *(const uint4*)((const uint16_t*)base + elem) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_or(float old, float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v), CTRL,
+                                                               0xf, 0xf, false));
+}
+
+// Prepares a chunk in four steps of about the same length, for the wave that
+// owns it; lane 16 g + q has token q and channels 32 h + 8 g + 0..7.  Places
+// past the sequence's end are neutral: decay 1, everything else 0.
+template <typename T>
+struct ChunkPrep {
+  uint4 raw[6][2];  // r, w, k, v, a, b
+  bool held;
+  float fall[16], grow[16], before[16];
+  uint4 at[3][2], rt[2][2], bt[3][2], kt[3][2];
+  float4v ab, ak, qb, qk;
+
+  __device__ __forceinline__ void load(const TimeMix& p, int head, int t0, int n, int lane) {
+    const int q = lane & 15, g = lane >> 4;
+    held = q < n;
+    const size_t at0 = (size_t)(t0 + q) * p.ld + head * kHead + 8 * g;
+    const void* src[6] = {p.r, p.w, p.k, p.v, p.a, p.b};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) raw[i][h] = block_or_zero(src[i], at0 + 32 * h, held);
+  }
+
+  __device__ __forceinline__ static void up8(uint4 v, float* f) {
+    up2<T>(v.x, f);
+    up2<T>(v.y, f + 2);
+    up2<T>(v.z, f + 4);
+    up2<T>(v.w, f + 6);
+  }
+
+  // accumulated decays: a sum over the 16 lanes of a row, then 2^L, 2^-L and
+  // the row before's 2^L
+  __device__ __forceinline__ void decays() {
+    float w[16];
+    up8(raw[1][0], w);
+    up8(raw[1][1], w + 8);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float l = held ? log2_decay(w[j]) : 0.f;
+      l += dpp<0x111>(l);  // row_shr:1, 2, 4, 8
+      l += dpp<0x112>(l);
+      l += dpp<0x114>(l);
+      l += dpp<0x118>(l);
+      fall[j] = __builtin_amdgcn_exp2f(l);
+      grow[j] = __builtin_amdgcn_exp2f(-l);
+      before[j] = dpp_or<0x111>(1.f, fall[j]);
+    }
+  }
+
+  __device__ __forceinline__ void factors() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 t[3];
+      float x[8];
+      auto scaled = [&](int which, const float* s) {
+        up8(raw[which][h], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= s[8 * h + j];
+      };
+      scaled(4, before);
+      split8<3>(x, t);
+      at[0][h] = t[0]; at[1][h] = t[1]; at[2][h] = t[2];
+      scaled(5, grow);
+      split8<3>(x, t);
+      bt[0][h] = t[0]; bt[1][h] = t[1]; bt[2][h] = t[2];
+      scaled(2, grow);
+      split8<3>(x, t);
+      kt[0][h] = t[0]; kt[1][h] = t[1]; kt[2][h] = t[2];
+      scaled(0, fall);
+      split8<2>(x, t);
+      rt[0][h] = t[0]; rt[1][h] = t[1];
+    }
+  }
+
+  // X Y^T over the 64 channels
+  template <int NT, int NX, int NY>
+  __device__ __forceinline__ static float4v gram(const uint4 (&x)[NX][2], const uint4 (&y)[NY][2]) {
+    float4v c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 a[NT], b[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        a[n] = x[n][h];
+        b[n] = y[n][h];
+      }
+      c = mul32<NT>(a, b, c);
+    }
+    return c;
+  }
+
+  __device__ __forceinline__ void grams() {
+    ab = gram<3>(at, bt);  // row t = 4 g + i, column s = q
+    ak = gram<3>(kt, at);  // row s = 4 g + i, column t = q: already the operand of Ak
+    qb = gram<2>(bt, rt);
+    qk = gram<2>(kt, rt);
+  }
+
+  __device__ __forceinline__ void put_rows(ChunkOps& o, int lane) const {
+    const int q = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int block = row_block(q, 4 * h + g);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) {
+        o.a[n][h][lane] = at[n][h];
+        o.b[n][block] = bt[n][h];
+        o.k[n][block] = kt[n][h];
+      }
+      o.r[0][h][lane] = rt[0][h];
+      o.r[1][h][lane] = rt[1][h];
+      put_v(o, block, raw[3][h], (T*)nullptr);
+      if (q == 15)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.end[32 * h + 8 * g + j] = fall[8 * h + j];
+    }
+  }
+  // V rows as bf16 terms: bf16 is one; fp16's eleven bits are two, exactly
+  __device__ __forceinline__ static void put_v(ChunkOps& o, int block, uint4 v, BF16*) { o.v[0][block] = v; }
+  __device__ __forceinline__ static void put_v(ChunkOps& o, int block, uint4 v, F16*) {
+    float x[8];
+    uint4 t[2];
+    up8(v, x);
+    split8<2>(x, t);
+    o.v[0][block] = t[0];
+    o.v[1][block] = t[1];
+  }
+
+  __device__ __forceinline__ static float lane_of(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  }
+  __device__ __forceinline__ static float4v pick4(const float* x, int g) {
+    float4v r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[i], b = x[4 + i], c = x[8 + i], d = x[12 + i];
+      const float lo = g & 1 ? b : a, hi = g & 1 ? d : c;
+      r[i] = g & 2 ? hi : lo;
+    }
+    return r;
+  }
+
+  // T = (1 - Ab)^-1 from T = 1 + T Ab: lane q has row q, and column s follows
+  // from the columns to its right.  Substitution, because the powers of Ab
+  // grow and cancel where neighbouring tokens share a direction.
+  __device__ __forceinline__ void solve(ChunkOps& o, int lane) const {
+    const int q = lane & 15, g = lane >> 4;
+    float row[16];
+#pragma unroll
+    for (int s = 15; s >= 0; --s) {
+      float x = q == s ? 1.f : 0.f;
+#pragma unroll
+      for (int u = 15; u > s; --u) x = fmaf(row[u], lane_of(ab[u & 3], 16 * (u >> 2) + s), x);
+      row[s] = x;
+    }
+    uint2 t[3];
+    split4<3>(pick4(row, g), t);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) o.t[n][lane] = t[n];
+    // slot s = 4 g + i of row t = q
+    float4v k = ak, qbm = qb, qkm = qk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = 4 * g + i;
+      if (s >= q) k[i] = 0.f;
+      if (s > q) qbm[i] = qkm[i] = 0.f;
+    }
+    split4<3>(k, t);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) o.ak[n][lane] = t[n];
+    uint2 b[2], c[2];
+    split4<2>(qbm, b);
+    split4<2>(qkm, c);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) o.q[n][lane] = make_uint4(b[n].x, b[n].y, c[n].x, c[n].y);
+  }
+};
+
+// The state's side of a chunk: sixteen channels of v per wave (16 wave + q),
+// S^T in four tiles.
+template <typename T>
+struct ChunkState {
+  float4v X[4];
+
+  __device__ __forceinline__ static int channel(int n, int g) { return 32 * (n >> 1) + 8 * g + 4 * (n & 1); }
+
+  __device__ __forceinline__ void load(const float* state, int wave, int lane) {
+    const int q = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      X[n] = state ? *(const float4v*)(state + (16 * wave + q) * kHead + channel(n, g)) : float4v{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void store(float* state, int wave, int lane) const {
+    const int q = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) *(float4v*)(state + (16 * wave + q) * kHead + channel(n, g)) = X[n];
+  }
+
+  // Takes the state over a chunk; returns Y (row t = 4 g + i, column v = q).
+  __device__ __forceinline__ float4v step(const ChunkOps& o, int wave, int lane) {
+    const int q = lane & 15, g = lane >> 4;
+    uint4 x[2][3];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = X[2 * h][i];
+        f[4 + i] = X[2 * h + 1][i];
+      }
+      split8<3>(f, x[h]);
+    }
+    constexpr int NV = __is_same(T, BF16) ? 1 : 2;
+    uint2 v[3] = {};
+#pragma unroll
+    for (int n = 0; n < NV; ++n) v[n] = rows4(o.v[n], g, q, 16 * wave + 4 * (q & 3));
+
+    // U = T (A S^T + Ak V)
+    float4v u0 = {0.f, 0.f, 0.f, 0.f}, u1 = u0, y = u0;
+    {
+      uint4 a[3];
+      uint2 k[3];
+#pragma unroll
+      for (int n = 0; n < 3; ++n) a[n] = o.a[n][0][lane];
+      u0 = mul32<3>(a, x[0], u0);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) k[n] = o.ak[n][lane];
+      if (NV == 2) {
+        u1 = mfma16(k[2], v[0], u1);
+        u1 = mfma16(k[1], v[1], u1);
+        u1 = mfma16(k[0], v[1], u1);
+      } else {
+        u1 = mfma16(k[2], v[0], u1);
+      }
+      u1 = mfma16(k[1], v[0], u1);
+      u1 = mfma16(k[0], v[0], u1);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) a[n] = o.a[n][1][lane];
+      u1 = mul32<3>(a, x[1], u1);
+    }
+    uint2 s[3], t[3];
+    split4<3>(u0 + u1, s);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) t[n] = o.t[n][lane];
+    float4v u = {0.f, 0.f, 0.f, 0.f};
+    u = mul16<3>(t, s, u);
+    // R S^T meanwhile
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 r[2] = {o.r[0][h][lane], o.r[1][h][lane]};
+      y = mul32<2>(r, x[h], y);
+    }
+    split4<3>(u, s);
+    uint4 uv[3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) uv[n] = make_uint4(s[n].x, s[n].y, v[n].x, v[n].y);
+    const uint4 qq[2] = {o.q[0][lane], o.q[1][lane]};
+    y = mul32<2>(qq, uv, y);
+    // S' = (S + U^T B + V^T K) diag(end)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      uint4 m[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const uint2 b = rows4(o.b[j], g, q, channel(n, q & 3)), k = rows4(o.k[j], g, q, channel(n, q & 3));
+        m[j] = make_uint4(b.x, b.y, k.x, k.y);
+      }
+      X[n] = mul32<3>(m, uv, X[n]);
+      X[n] *= *(const float4v*)&o.end[channel(n, g)];
+    }
+    return y;
+  }
+};
+
+}  // namespace rq

@@ -412,7 +412,7 @@ int rq_gemm_int8_acc(const int8_t *xq, int64_t m, const rq_qweight *w, int32_t *
  * Workspaces are as for the products; the split counters at their head are
  * neither read nor written.  None of these calls allocates or synchronizes,
  * and each gives the same bits for the same arguments.  nseq * heads and nseq
- * stay below 2^23, tokens * ld below 2^40.
+ * stay below 2^22, tokens * ld below 2^40.
  */
 
 /* The state recurrence, per head of 64 channels with a state S[64][64] (rows:
