@@ -92,66 +92,72 @@ __global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p) {
 
 // chunk kernel: one workgroup of eight waves per (sequence, head).  Waves 0-3
 // hold the state, sixteen channels of v each, and take it from chunk to chunk;
-// waves 4-7 prepare the chunks' operands, every fourth chunk each, in four
-// steps that they take one behind the other.  A barrier ends each step, in
-// which one chunk is finished and the one before it used: chunk c is written
-// in steps c + 2 and c + 3 into one of three LDS buffers and read in step
-// c + 4.  All eight waves pass chunks + 4 barriers.
+// waves 4-7 prepare the chunks' operands ahead of them, every fourth chunk
+// each, in an LDS buffer of their own.  Two counters per buffer order them:
+// `ready` chunks written, and `done` four per chunk read.  Every wait is for a
+// count that the other side reaches by itself: a buffer's chunk c waits for
+// the readers of chunk c - 4, who wait for nothing later than it.
 namespace {
-constexpr int kBuffers = 3;
 constexpr int kPreps = 4;
+
+struct ChunkLds {
+  ChunkOps ops[kPreps];
+  int ready[kPreps], done[kPreps];
+};
+
+__device__ __forceinline__ void wait_for(int* count, int want) {
+  while (__hip_atomic_load(count, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < want) __builtin_amdgcn_s_sleep(1);
+}
+__device__ __forceinline__ void signal(int* count, int lane) {
+  if (lane == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
 }  // namespace
 
 template <typename T>
 __global__ void __launch_bounds__(512) time_mix_chunk_kernel(TimeMix p) {
   extern __shared__ __align__(16) uint8_t lds[];
-  ChunkOps* ops = (ChunkOps*)lds;
+  ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, s = blockIdx.x / p.heads;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int begin, end;
   seq_span(p.seq, s, begin, end);
   const int chunks = (end - begin + kChunk - 1) / kChunk;
+  if (threadIdx.x < kPreps) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
+  __syncthreads();
   if (wave >= 4) {
     const int mine = wave - 4;
-    int steps = chunks + kPreps;
+    ChunkOps& o = sh.ops[mine];
     ChunkPrep<T> prep;
-    if (mine < chunks) prep.load(p, head, begin + mine * kChunk, min(kChunk, end - begin - mine * kChunk), lane);
-    for (int i = 0; i < mine && steps > 0; ++i, --steps) __syncthreads();
-    for (int c = mine; c < chunks; c += kPreps) {
-      ChunkOps& o = ops[c % kBuffers];
+    auto load = [&](int c) { prep.load(p, head, begin + c * kChunk, min(kChunk, end - begin - c * kChunk), lane); };
+    if (mine < chunks) load(mine);
+    int read = 0;
+    for (int c = mine; c < chunks; c += kPreps, read += 4) {
       prep.decays();
-      __syncthreads();
       prep.factors();
-      __syncthreads();
-      prep.put_rows(o, lane);
-      if (c + kPreps < chunks) {
-        const int t = (c + kPreps) * kChunk;
-        prep.load(p, head, begin + t, min(kChunk, end - begin - t), lane);
-      }
       prep.grams();
-      __syncthreads();
+      wait_for(&sh.done[mine], read);
+      prep.put_rows(o, lane);
+      if (c + kPreps < chunks) load(c + kPreps);
       prep.solve(o, lane);
-      __syncthreads();
-      steps -= kPreps;
+      signal(&sh.ready[mine], lane);
     }
-    for (; steps > 0; --steps) __syncthreads();
     return;
   }
   const int slot = slot_of(p.slots, s);
   const size_t state = ((size_t)(slot < 0 ? 0 : slot) * p.heads + head) * kHead * kHead;
   ChunkState<T> st;
   st.load(p.state_in && slot >= 0 ? p.state_in + state : nullptr, wave, lane);
-  for (int i = 0; i < kPreps; ++i) __syncthreads();
   const int q = lane & 15, g = lane >> 4;
   for (int c = 0; c < chunks; ++c) {
-    const float4v y = st.step(ops[c % kBuffers], wave, lane);
+    wait_for(&sh.ready[c % kPreps], c / kPreps + 1);
+    const float4v y = st.step(sh.ops[c % kPreps], wave, lane);
+    signal(&sh.done[c % kPreps], lane);
     const int t = begin + c * kChunk + 4 * g;
     uint16_t* to = (uint16_t*)p.y + (size_t)t * p.ldy + head * kHead + 16 * wave + q;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (t + i < end) to[(size_t)i * p.ldy] = (uint16_t)T::down2(y[i], 0.f);
-    __syncthreads();
   }
   if (p.state_out && slot >= 0) st.store(p.state_out + state, wave, lane);
 }
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(512) time_mix_chunk_kernel(TimeMix p) {
 namespace {
 template <typename T>
 hipError_t start_chunks(const TimeMix& p, hipStream_t st) {
-  constexpr int kLds = kBuffers * sizeof(ChunkOps);
+  constexpr int kLds = sizeof(ChunkLds);
   static const hipError_t attr = hipFuncSetAttribute((const void*)time_mix_chunk_kernel<T>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (attr != hipSuccess) return attr;
