@@ -131,6 +131,7 @@ size_t time_mix_back_bytes(int64_t tokens, int64_t heads, int64_t nseq);
 
 // 16-bit element types: widening is exact, narrowing rounds to nearest even
 struct F16 {
+  static constexpr uint32_t kMinusInf2 = 0xfc00fc00u;
   static __device__ __forceinline__ float up(uint32_t lo16) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)lo16);
   }
@@ -140,6 +141,7 @@ struct F16 {
   }
 };
 struct BF16 {
+  static constexpr uint32_t kMinusInf2 = 0xff80ff80u;
   static __device__ __forceinline__ float up(uint32_t lo16) { return __builtin_bit_cast(float, lo16 << 16); }
   static __device__ __forceinline__ uint32_t down2(float a, float b) {
     typedef __bf16 bf2 __attribute__((ext_vector_type(2)));

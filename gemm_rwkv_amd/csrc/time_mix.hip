@@ -90,86 +90,243 @@ __global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p) {
     for (int j = 0; j < 4; ++j) *(float4*)(p.state_out + state + (row + 4 * j) * kHead + col) = S[j];
 }
 
-// chunk kernel: one workgroup of eight waves per (sequence, head).  Waves 0-3
-// hold the state, sixteen channels of v each, and take it from chunk to chunk;
-// waves 4-7 prepare the chunks' operands ahead of them, every fourth chunk
-// each, in an LDS buffer of their own.  Two counters per buffer order them:
-// `ready` chunks written, and `done` four per chunk read.  Every wait is for a
-// count that the other side reaches by itself: a buffer's chunk c waits for
-// the readers of chunk c - 4, who wait for nothing later than it.
+// chunk kernel: one workgroup per (sequence, head).  Waves 0-3 hold the state,
+// sixteen channels of v each, and take it from chunk to chunk; the waves after
+// them prepare the chunks' operands ahead of them, in turn, in LDS buffers.
+// Two counters per buffer order them: `ready` chunks written, and `done` four
+// per chunk read.  Every wait is for a count that the other side reaches by
+// itself: a buffer's chunk c waits for the readers of chunk c - kBuffers, who
+// wait for nothing later than it.
 namespace {
-constexpr int kPreps = 4;
+constexpr int kBuffers = 4;
 
 struct ChunkLds {
-  ChunkOps ops[kPreps];
-  int ready[kPreps], done[kPreps];
+  ChunkOps ops[kBuffers];
+  int ready[kBuffers], done[kBuffers];
 };
 
+__device__ __forceinline__ int count_of(int* count) {
+  return __builtin_amdgcn_readfirstlane(__hip_atomic_load(count, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP));
+}
 __device__ __forceinline__ void wait_for(int* count, int want) {
-  while (__hip_atomic_load(count, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < want) __builtin_amdgcn_s_sleep(1);
+  while (count_of(count) < want) __builtin_amdgcn_s_sleep(1);
 }
 __device__ __forceinline__ void signal(int* count, int lane) {
   if (lane == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 }  // namespace
 
+// Where a workgroup is: a sequence, or a segment of one.
+//
+// A sequence is a chain of chunks, and few sequences and heads leave most of
+// the GPU idle.  Then each is cut into segments of `len` tokens.  The state
+// after a segment is S P + G, where G is what the segment leaves of a zero
+// state and P its map of the 64 channels of k; both are the recurrence itself,
+// started from zeros and from the identity (without v).  A first launch makes
+// G and P of every segment but the last ones, all at once (the first segment
+// starts from its real state and needs no P); in the second each segment
+// builds the state before it from those and then walks its chunks.
+struct SegmentSplit {
+  int len;        // tokens per segment, a multiple of 16; 0: whole sequences
+  float* states;  // [segments][heads][G, P][64][64]
+};
+
+namespace {
+struct Segment {
+  int seq, begin, end;
+  int nth, of;  // which of the sequence's segments
+};
+
+// Workgroup `idx`'s segment; false past the last one.
+__device__ __forceinline__ bool find_segment(const Sequences& s, int len, int idx, Segment& g) {
+  if (!len) {
+    g.seq = idx;
+    g.nth = 0;
+    g.of = 1;
+    seq_span(s, idx, g.begin, g.end);
+    return true;
+  }
+  for (int i = 0; i < s.nseq; ++i) {
+    int b, e;
+    seq_span(s, i, b, e);
+    const int n = max(1, (e - b + len - 1) / len);
+    if (idx < n) {
+      g.seq = i;
+      g.nth = idx;
+      g.of = n;
+      g.begin = b + idx * len;
+      g.end = min(e, g.begin + len);
+      return true;
+    }
+    idx -= n;
+  }
+  return false;
+}
+
+// The side of preparing wave `mine` of PREPS.
+template <typename T, int PREPS>
+__device__ __forceinline__ void prepare_chunks(const TimeMix& p, const Segment& g, ChunkLds& sh, int head, int mine, int lane) {
+  const int chunks = (g.end - g.begin + kChunk - 1) / kChunk;
+  ChunkPrep<T> prep;
+  for (int c = mine; c < chunks; c += PREPS) {
+    ChunkOps& o = sh.ops[c % kBuffers];
+    prep.load(p, head, g.begin + c * kChunk, min(kChunk, g.end - g.begin - c * kChunk), lane);
+    prep.decays();
+    // without these the scheduler mixes the stages and needs more registers
+    __builtin_amdgcn_sched_barrier(0);
+    prep.factors();
+    __builtin_amdgcn_sched_barrier(0);
+    prep.grams();
+    __builtin_amdgcn_sched_barrier(0);
+    wait_for(&sh.done[c % kBuffers], c / kBuffers * 4);
+    prep.put_rows(o, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    prep.solve(o, lane);
+    signal(&sh.ready[c % kBuffers], lane);
+  }
+}
+
+// The state's waves' side: NS states (see chunk_step) over the segment's
+// chunks; out(c, Y) takes each chunk's outputs.
+template <typename T, int NS, bool OUT, typename Out>
+__device__ __forceinline__ void walk_chunks(ChunkState* st, int chunks, ChunkLds& sh, int wave, int lane, Out out) {
+  ChunkHead<T> hd;
+  if (chunks > 0) {
+    wait_for(&sh.ready[0], 1);
+    hd.fetch(sh.ops[0], wave, lane);
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int n = c + 1;
+    const float4v y = chunk_step<T, NS, OUT>(st, sh.ops[c % kBuffers], hd, lane, [&] {
+      if (n < chunks) {
+        wait_for(&sh.ready[n % kBuffers], n / kBuffers + 1);
+        hd.fetch(sh.ops[n % kBuffers], wave, lane);
+      }
+    });
+    signal(&sh.done[c % kBuffers], lane);
+    if (OUT) out(c, y);
+  }
+}
+
+constexpr int kPreps = 8, kSegmentPreps = 8;
+}  // namespace
+
 template <typename T>
-__global__ void __launch_bounds__(512) time_mix_chunk_kernel(TimeMix p) {
+__global__ void __launch_bounds__(64 * (4 + kPreps)) time_mix_chunk_kernel(TimeMix p, SegmentSplit split) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
-  const int head = blockIdx.x % p.heads, s = blockIdx.x / p.heads;
+  const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int begin, end;
-  seq_span(p.seq, s, begin, end);
-  const int chunks = (end - begin + kChunk - 1) / kChunk;
-  if (threadIdx.x < kPreps) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
+  Segment sg;
+  if (!find_segment(p.seq, split.len, idx, sg)) return;
+  if (threadIdx.x < kBuffers) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
   __syncthreads();
   if (wave >= 4) {
-    const int mine = wave - 4;
-    ChunkOps& o = sh.ops[mine];
-    ChunkPrep<T> prep;
-    auto load = [&](int c) { prep.load(p, head, begin + c * kChunk, min(kChunk, end - begin - c * kChunk), lane); };
-    if (mine < chunks) load(mine);
-    int read = 0;
-    for (int c = mine; c < chunks; c += kPreps, read += 4) {
-      prep.decays();
-      prep.factors();
-      prep.grams();
-      wait_for(&sh.done[mine], read);
-      prep.put_rows(o, lane);
-      if (c + kPreps < chunks) load(c + kPreps);
-      prep.solve(o, lane);
-      signal(&sh.ready[mine], lane);
-    }
+    prepare_chunks<T, kPreps>(p, sg, sh, head, wave - 4, lane);
     return;
   }
-  const int slot = slot_of(p.slots, s);
+  const int slot = slot_of(p.slots, sg.seq);
   const size_t state = ((size_t)(slot < 0 ? 0 : slot) * p.heads + head) * kHead * kHead;
-  ChunkState<T> st;
-  st.load(p.state_in && slot >= 0 ? p.state_in + state : nullptr, wave, lane);
-  const int q = lane & 15, g = lane >> 4;
-  for (int c = 0; c < chunks; ++c) {
-    wait_for(&sh.ready[c % kPreps], c / kPreps + 1);
-    const float4v y = st.step(sh.ops[c % kPreps], wave, lane);
-    signal(&sh.done[c % kPreps], lane);
-    const int t = begin + c * kChunk + 4 * g;
-    uint16_t* to = (uint16_t*)p.y + (size_t)t * p.ldy + head * kHead + 16 * wave + q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (t + i < end) to[(size_t)i * p.ldy] = (uint16_t)T::down2(y[i], 0.f);
+  ChunkState st;
+  if (sg.of == 1) {
+    st.load(p.state_in && slot >= 0 ? p.state_in + state : nullptr, wave, lane);
+  } else {
+    // The segments of this sequence begin at workgroup idx - nth.  The first
+    // one's P holds the sequence's own state: state_out may be state_in, and
+    // the last segment may be done before the first one starts.
+    const size_t pair = 2 * kHead * kHead, stride = p.heads * pair;
+    const float* at = split.states + (size_t)(idx - sg.nth) * stride + head * pair;
+    st.load(sg.nth ? at : at + kHead * kHead, wave, lane);
+    for (int i = 1; i < sg.nth; ++i) st.apply(at + i * stride, at + i * stride + kHead * kHead, wave, lane);
   }
-  if (p.state_out && slot >= 0) st.store(p.state_out + state, wave, lane);
+  const int chunks = (sg.end - sg.begin + kChunk - 1) / kChunk;
+  const int q = lane & 15, g = lane >> 4;
+  uint16_t* to = (uint16_t*)p.y + (size_t)(sg.begin + 4 * g) * p.ldy + head * kHead + 16 * wave + q;
+  walk_chunks<T, 1, true>(&st, chunks, sh, wave, lane, [&](int c, float4v y) {
+    const int left = sg.end - sg.begin - c * kChunk;
+    const uint32_t y01 = T::down2(y[0], y[1]), y23 = T::down2(y[2], y[3]);
+    if (left >= kChunk) {
+      to[0] = (uint16_t)y01;
+      to[p.ldy] = (uint16_t)(y01 >> 16);
+      to[2 * (size_t)p.ldy] = (uint16_t)y23;
+      to[3 * (size_t)p.ldy] = (uint16_t)(y23 >> 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * g + i < left) to[(size_t)i * p.ldy] = (uint16_t)((i < 2 ? y01 : y23) >> (16 * (i & 1)));
+    }
+    to += (size_t)kChunk * p.ldy;
+  });
+  if (p.state_out && slot >= 0 && sg.nth + 1 == sg.of) st.store(p.state_out + state, wave, lane);
+}
+
+// G and P of a segment; of a first one the state after it, and before it.
+template <typename T>
+__global__ void __launch_bounds__(64 * (4 + kSegmentPreps)) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  ChunkLds& sh = *(ChunkLds*)lds;
+  const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Segment sg;
+  if (!find_segment(p.seq, split.len, idx, sg) || sg.nth + 1 == sg.of) return;
+  if (threadIdx.x < kBuffers) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
+  __syncthreads();
+  if (wave >= 4) {
+    prepare_chunks<T, kSegmentPreps>(p, sg, sh, head, wave - 4, lane);
+    return;
+  }
+  const int slot = slot_of(p.slots, sg.seq);
+  const int chunks = (sg.end - sg.begin) / kChunk;  // whole: only a last segment is ragged
+  auto none = [](int, float4v) {};
+  float* to = split.states + ((size_t)idx * p.heads + head) * 2 * kHead * kHead;
+  ChunkState st[2];
+  if (sg.nth == 0) {
+    st[0].load(p.state_in && slot >= 0 ? p.state_in + ((size_t)slot * p.heads + head) * kHead * kHead : nullptr, wave, lane);
+    st[0].store(to + kHead * kHead, wave, lane);
+    walk_chunks<T, 1, false>(st, chunks, sh, wave, lane, none);
+  } else {
+    st[0].load(nullptr, wave, lane);
+    st[1].identity(wave, lane);
+    walk_chunks<T, 2, false>(st, chunks, sh, wave, lane, none);
+    st[1].store(to + kHead * kHead, wave, lane);
+  }
+  st[0].store(to, wave, lane);
 }
 
 namespace {
+template <typename K>
+hipError_t allow_lds(K* kernel) {
+  return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(ChunkLds));
+}
+
+// Tokens per segment, or 0 for none.  A cut sequence costs about 2.4 times
+// the work, so it pays only from four segments on; they are made to fill the
+// 256 compute units once, and are at least 128 tokens long.
+int segment_len(const TimeMix& p) {
+  const int64_t chains = (int64_t)p.seq.nseq * p.heads;
+  const int64_t mean = p.seq.tokens / p.seq.nseq;
+  const int64_t want = 256 / chains;
+  if (want < 4 || mean < 4 * 128) return 0;
+  int64_t len = (mean + want - 1) / want;
+  if (len < 128) len = 128;
+  len = (len + kChunk - 1) / kChunk * kChunk;
+  const int64_t segments = p.seq.tokens / len + p.seq.nseq;
+  if (!p.parts || (size_t)segments * p.heads * 2 * kHead * kHead * 4 > p.parts_bytes) return 0;
+  return (int)len;
+}
+
 template <typename T>
 hipError_t start_chunks(const TimeMix& p, hipStream_t st) {
-  constexpr int kLds = sizeof(ChunkLds);
-  static const hipError_t attr = hipFuncSetAttribute((const void*)time_mix_chunk_kernel<T>,
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3((unsigned)p.seq.nseq * p.heads), dim3(512), kLds, st, p);
+  static const hipError_t attr = allow_lds(time_mix_chunk_kernel<T>);
+  static const hipError_t attr2 = allow_lds(time_mix_segment_kernel<T>);
+  if (attr != hipSuccess || attr2 != hipSuccess) return attr != hipSuccess ? attr : attr2;
+  SegmentSplit split = {segment_len(p), p.parts};
+  const unsigned chains = (unsigned)(split.len ? p.seq.tokens / split.len + p.seq.nseq : p.seq.nseq) * p.heads;
+  if (split.len)
+    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(64 * (4 + kSegmentPreps)), sizeof(ChunkLds), st, p, split);
+  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(64 * (4 + kPreps)), sizeof(ChunkLds), st, p, split);
   return hipGetLastError();
 }
 }  // namespace

@@ -37,10 +37,6 @@ constexpr int kChunk = 16;
 __device__ __forceinline__ float4v mfma32(uint4 a, uint4 b, float4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ float4v mfma16(uint2 a, uint2 b, float4v c) {
-  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, a), __builtin_bit_cast(short4v, b), c, 0, 0, 0);
-}
-
 // the upper halves of two words: a bf16 pair, cut (not rounded)
 __device__ __forceinline__ uint32_t high2(float lo, float hi) {
   return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
@@ -98,16 +94,24 @@ __device__ __forceinline__ float4v mul32(const uint4* a, const uint4* b, float4v
   c = mfma32(a[1], b[0], c);
   return mfma32(a[0], b[0], c);
 }
-template <int NT>
-__device__ __forceinline__ float4v mul16(const uint2* a, const uint2* b, float4v c) {
-  if (NT == 3) {
-    c = mfma16(a[0], b[2], c);
-    c = mfma16(a[2], b[0], c);
-    c = mfma16(a[1], b[1], c);
-  }
-  c = mfma16(a[0], b[1], c);
-  c = mfma16(a[1], b[0], c);
-  return mfma16(a[0], b[0], c);
+
+__device__ __forceinline__ uint4 pair(uint2 a, uint2 b) { return make_uint4(a.x, a.y, b.x, b.y); }
+
+// A product over 16 tokens fills half of an instruction's 32 slots, so two
+// term products go side by side: (a0, a1) with (b0, b0) and so on.  The
+// 16-slot instruction is not used: it takes as long, and its result as the
+// addend of a 32-slot one came out without its last two registers at times.
+__device__ __forceinline__ float4v mul_tokens(const uint2* a, const uint2* b, float4v c) {
+  c = mfma32(pair(a[0], a[2]), pair(b[2], b[0]), c);
+  c = mfma32(pair(a[0], a[1]), pair(b[1], b[1]), c);
+  return mfma32(pair(a[0], a[1]), pair(b[0], b[0]), c);
+}
+// the same with NV exact terms of b
+template <int NV>
+__device__ __forceinline__ float4v mul_values(const uint2* a, const uint2* b, float4v c) {
+  c = mfma32(pair(a[2], make_uint2(0, 0)), pair(b[0], make_uint2(0, 0)), c);
+  if (NV == 2) c = mfma32(pair(a[0], a[1]), pair(b[NV - 1], b[NV - 1]), c);
+  return mfma32(pair(a[0], a[1]), pair(b[0], b[0]), c);
 }
 
 // One chunk's operands in LDS, prepared by one wave and read by those that
@@ -138,9 +142,9 @@ __device__ __forceinline__ uint2 rows4(const uint4* rows, int g, int q, int chan
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p));
 }
 
-// One 16-byte block of row t, or zeros past the sequence's end.
-__device__ __forceinline__ uint4 block_or_zero(const void* base, size_t elem, bool held) {
-  return held ? *(const uint4*)((const uint16_t*)base + elem) : make_uint4(0u, 0u, 0u, 0u);
+// One 16-byte block of a row, or a constant past the sequence's end.
+__device__ __forceinline__ uint4 block_or(uint32_t other, const void* base, size_t elem, bool held) {
+  return held ? *(const uint4*)((const uint16_t*)base + elem) : make_uint4(other, other, other, other);
 }
 
 template <int CTRL>
@@ -151,24 +155,24 @@ __device__ __forceinline__ float dpp_or(float old, float v) {
 
 // Prepares a chunk in four steps of about the same length, for the wave that
 // owns it; lane 16 g + q has token q and channels 32 h + 8 g + 0..7.  Places
-// past the sequence's end are neutral: decay 1, everything else 0.
+// past the sequence's end are neutral: a raw decay of -inf, which is a decay
+// of 1, and zeros everywhere else.
 template <typename T>
 struct ChunkPrep {
   uint4 raw[6][2];  // r, w, k, v, a, b
-  bool held;
   float fall[16], grow[16], before[16];
   uint4 at[3][2], rt[2][2], bt[3][2], kt[3][2];
   float4v ab, ak, qb, qk;
 
   __device__ __forceinline__ void load(const TimeMix& p, int head, int t0, int n, int lane) {
     const int q = lane & 15, g = lane >> 4;
-    held = q < n;
+    const bool held = q < n;
     const size_t at0 = (size_t)(t0 + q) * p.ld + head * kHead + 8 * g;
     const void* src[6] = {p.r, p.w, p.k, p.v, p.a, p.b};
 #pragma unroll
     for (int i = 0; i < 6; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) raw[i][h] = block_or_zero(src[i], at0 + 32 * h, held);
+      for (int h = 0; h < 2; ++h) raw[i][h] = block_or(i == 1 ? T::kMinusInf2 : 0u, src[i], at0 + 32 * h, held);
   }
 
   __device__ __forceinline__ static void up8(uint4 v, float* f) {
@@ -186,7 +190,7 @@ struct ChunkPrep {
     up8(raw[1][1], w + 8);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      float l = held ? log2_decay(w[j]) : 0.f;
+      float l = log2_decay(w[j]);
       l += dpp<0x111>(l);  // row_shr:1, 2, 4, 8
       l += dpp<0x112>(l);
       l += dpp<0x114>(l);
@@ -328,7 +332,6 @@ struct ChunkPrep {
 
 // The state's side of a chunk: sixteen channels of v per wave (16 wave + q),
 // S^T in four tiles.
-template <typename T>
 struct ChunkState {
   float4v X[4];
 
@@ -345,81 +348,141 @@ struct ChunkState {
 #pragma unroll
     for (int n = 0; n < 4; ++n) *(float4v*)(state + (16 * wave + q) * kHead + channel(n, g)) = X[n];
   }
-
-  // Takes the state over a chunk; returns Y (row t = 4 g + i, column v = q).
-  __device__ __forceinline__ float4v step(const ChunkOps& o, int wave, int lane) {
+  // rows of the identity, for the map from the state before a segment to the
+  // one after it
+  __device__ __forceinline__ void identity(int wave, int lane) {
     const int q = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[n][i] = channel(n, g) + i == 16 * wave + q ? 1.f : 0.f;
+  }
+
+  // S <- S P + G with P, G [64][64] in fp32, on fp32 matrix instructions:
+  // register i of tile n is the slot of contraction channel(n, g) + i.
+  __device__ __forceinline__ void apply(const float* G, const float* P, int wave, int lane) {
+    const int q = lane & 15, g = lane >> 4;
+    ChunkState to;
+    to.load(G, wave, lane);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float* row = P + 32 * (m >> 1) + 8 * (q >> 2) + 4 * (m & 1) + (q & 3);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to.X[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[(channel(n, g) + i) * kHead], X[n][i], to.X[m], 0, 0, 0);
+    }
+    *this = to;
+  }
+};
+
+// The operands that a chunk starts with.
+template <typename T>
+struct ChunkHead {
+  static constexpr int kV = __is_same(T, BF16) ? 1 : 2;  // terms of V
+  uint4 a[2][3];
+  uint2 ak[3], v[kV], t[3];
+
+  __device__ __forceinline__ void fetch(const ChunkOps& o, int wave, int lane) {
+    const int q = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) a[h][n] = o.a[n][h][lane];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) ak[n] = o.ak[n][lane];
+#pragma unroll
+    for (int n = 0; n < kV; ++n) v[n] = rows4(o.v[n], g, q, 16 * wave + 4 * (q & 3));
+#pragma unroll
+    for (int n = 0; n < 3; ++n) t[n] = o.t[n][lane];
+  }
+};
+
+// Takes NS states over a chunk: the first with V, the second, if there is one,
+// without (the map alone).  OUT: Y of the first (row t = 4 g + i, column v = q).
+//
+// What bounds it: the four waves' reads of the operands, 26 KB each, take the
+// LDS about as long as the products take the matrix units.  So they are
+// fetched ahead by hand, each stage's under the stage before: R and Q while
+// the state is cut into terms, B and K while U is made, and the next chunk's
+// A, Ak, V and T (`next`) under the state's update.
+template <typename T, int NS, bool OUT, typename Next>
+__device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o, ChunkHead<T>& hd, int lane, Next next) {
+  const int q = lane & 15, g = lane >> 4;
+  constexpr int NV = ChunkHead<T>::kV;
+  const float4v zero = {0.f, 0.f, 0.f, 0.f};
+  uint4 r[2][2], qq[2];
+  if (OUT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) r[h][n] = o.r[n][h][lane];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) qq[n] = o.q[n][lane];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  float4v u[NS], y = zero;
+#pragma unroll
+  for (int m = 0; m < NS; ++m) {
+    // U = T (A S^T + Ak V), and R S^T
     uint4 x[2][3];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[i] = X[2 * h][i];
-        f[4 + i] = X[2 * h + 1][i];
+        f[i] = st[m].X[2 * h][i];
+        f[4 + i] = st[m].X[2 * h + 1][i];
       }
       split8<3>(f, x[h]);
     }
-    constexpr int NV = __is_same(T, BF16) ? 1 : 2;
-    uint2 v[3] = {};
+    float4v u0 = mul32<3>(hd.a[0], x[0], zero), u1 = zero;
+    if (m == 0) u1 = mul_values<NV>(hd.ak, hd.v, u1);
+    u1 = mul32<3>(hd.a[1], x[1], u1);
+    u[m] = u0 + u1;
+    if (OUT && m == 0)
 #pragma unroll
-    for (int n = 0; n < NV; ++n) v[n] = rows4(o.v[n], g, q, 16 * wave + 4 * (q & 3));
-
-    // U = T (A S^T + Ak V)
-    float4v u0 = {0.f, 0.f, 0.f, 0.f}, u1 = u0, y = u0;
-    {
-      uint4 a[3];
-      uint2 k[3];
-#pragma unroll
-      for (int n = 0; n < 3; ++n) a[n] = o.a[n][0][lane];
-      u0 = mul32<3>(a, x[0], u0);
-#pragma unroll
-      for (int n = 0; n < 3; ++n) k[n] = o.ak[n][lane];
-      if (NV == 2) {
-        u1 = mfma16(k[2], v[0], u1);
-        u1 = mfma16(k[1], v[1], u1);
-        u1 = mfma16(k[0], v[1], u1);
-      } else {
-        u1 = mfma16(k[2], v[0], u1);
-      }
-      u1 = mfma16(k[1], v[0], u1);
-      u1 = mfma16(k[0], v[0], u1);
-#pragma unroll
-      for (int n = 0; n < 3; ++n) a[n] = o.a[n][1][lane];
-      u1 = mul32<3>(a, x[1], u1);
-    }
-    uint2 s[3], t[3];
-    split4<3>(u0 + u1, s);
-#pragma unroll
-    for (int n = 0; n < 3; ++n) t[n] = o.t[n][lane];
-    float4v u = {0.f, 0.f, 0.f, 0.f};
-    u = mul16<3>(t, s, u);
-    // R S^T meanwhile
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 r[2] = {o.r[0][h][lane], o.r[1][h][lane]};
-      y = mul32<2>(r, x[h], y);
-    }
-    split4<3>(u, s);
-    uint4 uv[3];
-#pragma unroll
-    for (int n = 0; n < 3; ++n) uv[n] = make_uint4(s[n].x, s[n].y, v[n].x, v[n].y);
-    const uint4 qq[2] = {o.q[0][lane], o.q[1][lane]};
-    y = mul32<2>(qq, uv, y);
-    // S' = (S + U^T B + V^T K) diag(end)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      uint4 m[3];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const uint2 b = rows4(o.b[j], g, q, channel(n, q & 3)), k = rows4(o.k[j], g, q, channel(n, q & 3));
-        m[j] = make_uint4(b.x, b.y, k.x, k.y);
-      }
-      X[n] = mul32<3>(m, uv, X[n]);
-      X[n] *= *(const float4v*)&o.end[channel(n, g)];
-    }
-    return y;
+      for (int h = 0; h < 2; ++h) y = mul32<2>(r[h], x[h], y);
   }
-};
+  __builtin_amdgcn_sched_barrier(0);
+  uint2 b[4][3], k[4][3];
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      b[n][j] = rows4(o.b[j], g, q, ChunkState::channel(n, q & 3));
+      k[n][j] = rows4(o.k[j], g, q, ChunkState::channel(n, q & 3));
+    }
+  __builtin_amdgcn_sched_barrier(0);
+  uint2 s[NS][3];
+#pragma unroll
+  for (int m = 0; m < NS; ++m) {
+    split4<3>(u[m], s[m]);
+    u[m] = mul_tokens(hd.t, s[m], zero);
+    split4<3>(u[m], s[m]);
+  }
+  // S' = (S + U^T B + V^T K) diag(end), Y = R S^T + Q (U, V)
+  uint4 uv[NS][3];
+#pragma unroll
+  for (int n = 0; n < 3; ++n) {
+    uv[0][n] = pair(s[0][n], n < NV ? hd.v[n < NV ? n : 0] : make_uint2(0, 0));
+    if (NS > 1) uv[NS - 1][n] = pair(s[NS - 1][n], make_uint2(0, 0));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  next();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const float4v end = *(const float4v*)&o.end[ChunkState::channel(n, g)];
+    uint4 c[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) c[j] = pair(b[n][j], k[n][j]);
+#pragma unroll
+    for (int m = 0; m < NS; ++m) st[m].X[n] = mul32<3>(c, uv[m], st[m].X[n]) * end;
+  }
+  if (OUT) y = mul32<2>(qq, uv[0], y);
+  return y;
+}
 
 }  // namespace rq
