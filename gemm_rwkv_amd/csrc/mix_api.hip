@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t kMostWidth = 8192;  // a row is held in the registers of one workgroup
 constexpr int64_t kMostMix = 8;
-constexpr int64_t kMostGrid = (int64_t)1 << 22;  // workgroups of one launch
+constexpr int64_t kMostGrid = (int64_t)1 << 21;  // workgroups of one launch
 
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
@@ -193,7 +193,7 @@ int rq_time_mix_backward(int dtype, const void* r, const void* w, const void* k,
   if ((st = check_type(dtype)) != RQ_OK) return st;
   if ((st = check_heads(tokens, heads, ld)) != RQ_OK) return st;
   if ((st = check_seqs(tokens, cu, nseq)) != RQ_OK) return st;
-  if (nseq * heads >= kMostGrid) return RQ_ERR_SHAPE;
+  if (nseq * heads >= kMostGrid || (tokens / 16 + nseq) * heads >= ((int64_t)1 << 24)) return RQ_ERR_SHAPE;
   const int64_t width = heads * rq::kHead;
   Buffers io;
   const void* rows[7] = {r, w, k, v, a, b, dy};

@@ -90,32 +90,6 @@ __global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p) {
     for (int j = 0; j < 4; ++j) *(float4*)(p.state_out + state + (row + 4 * j) * kHead + col) = S[j];
 }
 
-// chunk kernel: one workgroup per (sequence, head).  Waves 0-3 hold the state,
-// sixteen channels of v each, and take it from chunk to chunk; the waves after
-// them prepare the chunks' operands ahead of them, in turn, in LDS buffers.
-// Two counters per buffer order them: `ready` chunks written, and `done` four
-// per chunk read.  Every wait is for a count that the other side reaches by
-// itself: a buffer's chunk c waits for the readers of chunk c - kBuffers, who
-// wait for nothing later than it.
-namespace {
-constexpr int kBuffers = 4;
-
-struct ChunkLds {
-  ChunkOps ops[kBuffers];
-  int ready[kBuffers], done[kBuffers];
-};
-
-__device__ __forceinline__ int count_of(int* count) {
-  return __builtin_amdgcn_readfirstlane(__hip_atomic_load(count, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP));
-}
-__device__ __forceinline__ void wait_for(int* count, int want) {
-  while (count_of(count) < want) __builtin_amdgcn_s_sleep(1);
-}
-__device__ __forceinline__ void signal(int* count, int lane) {
-  if (lane == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
-}
-}  // namespace
-
 // Where a workgroup is: a sequence, or a segment of one.
 //
 // A sequence is a chain of chunks, and few sequences and heads leave most of
@@ -163,56 +137,10 @@ __device__ __forceinline__ bool find_segment(const Sequences& s, int len, int id
   return false;
 }
 
-// The side of preparing wave `mine` of PREPS.
-template <typename T, int PREPS>
-__device__ __forceinline__ void prepare_chunks(const TimeMix& p, const Segment& g, ChunkLds& sh, int head, int mine, int lane) {
-  const int chunks = (g.end - g.begin + kChunk - 1) / kChunk;
-  ChunkPrep<T> prep;
-  for (int c = mine; c < chunks; c += PREPS) {
-    ChunkOps& o = sh.ops[c % kBuffers];
-    prep.load(p, head, g.begin + c * kChunk, min(kChunk, g.end - g.begin - c * kChunk), lane);
-    prep.decays();
-    // without these the scheduler mixes the stages and needs more registers
-    __builtin_amdgcn_sched_barrier(0);
-    prep.factors();
-    __builtin_amdgcn_sched_barrier(0);
-    prep.grams();
-    __builtin_amdgcn_sched_barrier(0);
-    wait_for(&sh.done[c % kBuffers], c / kBuffers * 4);
-    prep.put_rows(o, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    prep.solve(o, lane);
-    signal(&sh.ready[c % kBuffers], lane);
-  }
-}
-
-// The state's waves' side: NS states (see chunk_step) over the segment's
-// chunks; out(c, Y) takes each chunk's outputs.
-template <typename T, int NS, bool OUT, typename Out>
-__device__ __forceinline__ void walk_chunks(ChunkState* st, int chunks, ChunkLds& sh, int wave, int lane, Out out) {
-  ChunkHead<T> hd;
-  if (chunks > 0) {
-    wait_for(&sh.ready[0], 1);
-    hd.fetch(sh.ops[0], wave, lane);
-  }
-  for (int c = 0; c < chunks; ++c) {
-    const int n = c + 1;
-    const float4v y = chunk_step<T, NS, OUT>(st, sh.ops[c % kBuffers], hd, lane, [&] {
-      if (n < chunks) {
-        wait_for(&sh.ready[n % kBuffers], n / kBuffers + 1);
-        hd.fetch(sh.ops[n % kBuffers], wave, lane);
-      }
-    });
-    signal(&sh.done[c % kBuffers], lane);
-    if (OUT) out(c, y);
-  }
-}
-
-constexpr int kPreps = 8, kSegmentPreps = 8;
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(64 * (4 + kPreps)) time_mix_chunk_kernel(TimeMix p, SegmentSplit split) {
+__global__ void __launch_bounds__(kWalkThreads) time_mix_chunk_kernel(TimeMix p, SegmentSplit split) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
@@ -220,10 +148,9 @@ __global__ void __launch_bounds__(64 * (4 + kPreps)) time_mix_chunk_kernel(TimeM
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Segment sg;
   if (!find_segment(p.seq, split.len, idx, sg)) return;
-  if (threadIdx.x < kBuffers) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
-  __syncthreads();
+  clear_counts(sh);
   if (wave >= 4) {
-    prepare_chunks<T, kPreps>(p, sg, sh, head, wave - 4, lane);
+    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
     return;
   }
   const int slot = slot_of(p.slots, sg.seq);
@@ -243,7 +170,7 @@ __global__ void __launch_bounds__(64 * (4 + kPreps)) time_mix_chunk_kernel(TimeM
   const int chunks = (sg.end - sg.begin + kChunk - 1) / kChunk;
   const int q = lane & 15, g = lane >> 4;
   uint16_t* to = (uint16_t*)p.y + (size_t)(sg.begin + 4 * g) * p.ldy + head * kHead + 16 * wave + q;
-  walk_chunks<T, 1, true>(&st, chunks, sh, wave, lane, [&](int c, float4v y) {
+  walk_chunks<T, 1, true, false>(&st, chunks, sh, wave, lane, [](int) {}, [](int, float4v) {}, [&](int c, float4v y) {
     const int left = sg.end - sg.begin - c * kChunk;
     const uint32_t y01 = T::down2(y[0], y[1]), y23 = T::down2(y[2], y[3]);
     if (left >= kChunk) {
@@ -263,7 +190,7 @@ __global__ void __launch_bounds__(64 * (4 + kPreps)) time_mix_chunk_kernel(TimeM
 
 // G and P of a segment; of a first one the state after it, and before it.
 template <typename T>
-__global__ void __launch_bounds__(64 * (4 + kSegmentPreps)) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
+__global__ void __launch_bounds__(kWalkThreads) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
@@ -271,10 +198,9 @@ __global__ void __launch_bounds__(64 * (4 + kSegmentPreps)) time_mix_segment_ker
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Segment sg;
   if (!find_segment(p.seq, split.len, idx, sg) || sg.nth + 1 == sg.of) return;
-  if (threadIdx.x < kBuffers) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
-  __syncthreads();
+  clear_counts(sh);
   if (wave >= 4) {
-    prepare_chunks<T, kSegmentPreps>(p, sg, sh, head, wave - 4, lane);
+    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
     return;
   }
   const int slot = slot_of(p.slots, sg.seq);
@@ -285,22 +211,17 @@ __global__ void __launch_bounds__(64 * (4 + kSegmentPreps)) time_mix_segment_ker
   if (sg.nth == 0) {
     st[0].load(p.state_in && slot >= 0 ? p.state_in + ((size_t)slot * p.heads + head) * kHead * kHead : nullptr, wave, lane);
     st[0].store(to + kHead * kHead, wave, lane);
-    walk_chunks<T, 1, false>(st, chunks, sh, wave, lane, none);
+    walk_chunks<T, 1, false, false>(st, chunks, sh, wave, lane, [](int) {}, none, none);
   } else {
     st[0].load(nullptr, wave, lane);
     st[1].identity(wave, lane);
-    walk_chunks<T, 2, false>(st, chunks, sh, wave, lane, none);
+    walk_chunks<T, 2, false, false>(st, chunks, sh, wave, lane, [](int) {}, none, none);
     st[1].store(to + kHead * kHead, wave, lane);
   }
   st[0].store(to, wave, lane);
 }
 
 namespace {
-template <typename K>
-hipError_t allow_lds(K* kernel) {
-  return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(ChunkLds));
-}
-
 // Tokens per segment, or 0 for none.  A cut sequence costs about 2.4 times
 // the work, so it pays only from four segments on; they are made to fill the
 // 256 compute units once, and are at least 128 tokens long.
@@ -325,8 +246,8 @@ hipError_t start_chunks(const TimeMix& p, hipStream_t st) {
   SegmentSplit split = {segment_len(p), p.parts};
   const unsigned chains = (unsigned)(split.len ? p.seq.tokens / split.len + p.seq.nseq : p.seq.nseq) * p.heads;
   if (split.len)
-    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(64 * (4 + kSegmentPreps)), sizeof(ChunkLds), st, p, split);
-  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(64 * (4 + kPreps)), sizeof(ChunkLds), st, p, split);
+    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(kWalkThreads), sizeof(ChunkLds), st, p, split);
+  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(kWalkThreads), sizeof(ChunkLds), st, p, split);
   return hipGetLastError();
 }
 }  // namespace

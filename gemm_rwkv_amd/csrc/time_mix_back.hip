@@ -1,181 +1,447 @@
-// Gradient of the state recurrence.  Walking back from dS = dstate_out, with
-// u = S_{t-1} a:
+// Gradient of the state recurrence, in chunks of 16 tokens (time_mix_chunk.h
+// for the chunk's products and the notation).
 //
-//   dS += dy r^T,  dr = S_t^T dy,  dk = dS^T v,  dv = dS k,  db = dS^T u,
-//   du = dS b,  da = S_{t-1}^T du,  dw_j = sum_i dS_ij S_{t-1},ij,
-//   dS_{t-1} = dS diag(w) + du a^T,  draw = dw w (-exp(-1/2)) s (1 - s)
+// Two chains run along each sequence, independent of each other: the state S
+// forward, and the gradient E of the state back.  The first launch walks both
+// at once, a workgroup each, and leaves for every chunk the state before it,
+// D = E diag(exp L_15) after it, U and Z.  With those the chunks no longer
+// depend on each other, and the second launch makes the gradients of all of
+// them at once:
 //
-// with s = sigmoid(raw).  One workgroup per (sequence, head).  A forward pass
-// leaves the state before every run of 16 tokens in the workspace; the walk
-// back computes the states within each run again into a second part of it.
+//   dQb = tril(dY U^T)   dQk = tril(dY V^T)   dAb, dAk = strictly lower Z U^T, Z V^T
+//   dR = dY S + dQb B + dQk K        dA = Z S + dAb B + dAk K
+//   dB = U D + dQb^T R + dAb^T A     dK = V D + dQk^T R + dAk^T A
+//   dV = Qk^T dY + Ak^T Z + K D^T
+//
+// each times the decay that scaled its input, and for the decays
+//   dL_t = R dR - B dB - K dK + (A dA)_{t+1},
+//   dL_15 = ... + sum_v D o (S + U^T B + V^T K),   dlog w_t = sum_{s>=t} dL_s.
+// What a token reads of itself (the diagonals of dQb and dQk) is in R dR and in
+// B dB and K dK alike and no decay lies between: it is added after dL, so that
+// it cancels exactly.
 #include "mix.h"
+#include "time_mix_chunk.h"
 
 namespace rq {
 
 namespace {
-constexpr int kRun = 16;
 constexpr int kState = kHead * kHead;
 
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x)));
+// Chunk c of sequence s is number begin / 16 + s + c of all chunks: at least
+// one past every chunk of the sequences before it.
+__device__ __forceinline__ int first_chunk(int begin, int s) { return begin / kChunk + s; }
+
+// The sequence of chunk number j, and its place there; false for a number
+// between two sequences.
+__device__ __forceinline__ bool find_chunk(const Sequences& q, int j, int& begin, int& end, int& c) {
+  int lo = 0, hi = q.nseq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    seq_span(q, mid, begin, end);
+    if (first_chunk(begin, mid) <= j) lo = mid; else hi = mid - 1;
+  }
+  seq_span(q, lo, begin, end);
+  c = j - first_chunk(begin, lo);
+  return c >= 0 && c < (end - begin + kChunk - 1) / kChunk;
 }
-__device__ __forceinline__ float4 axpy4(float a, float4 x, float4 y) {
-  return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
-}
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-}
-// over the four row groups of a wave
-__device__ __forceinline__ float4 cols_sum(float4 v) {
-  v.x += __shfl_xor(v.x, 16); v.y += __shfl_xor(v.y, 16); v.z += __shfl_xor(v.z, 16); v.w += __shfl_xor(v.w, 16);
-  v.x += __shfl_xor(v.x, 32); v.y += __shfl_xor(v.y, 32); v.z += __shfl_xor(v.z, 32); v.w += __shfl_xor(v.w, 32);
-  return v;
-}
+
+// What the chains leave per chunk and head.
+struct Chain {
+  float* S;  // [chunks][heads][64 v][64 k]
+  float* D;
+  float* U;  // [chunks][heads][16 t][64 v]
+  float* Z;
+};
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(256) time_mix_back_kernel(TimeMixBack b) {
-  const TimeMix& p = b.f;
-  __shared__ __align__(16) float in[7][kRun][kHead];       // r, decay, k, v, a, b, dy
-  __shared__ __align__(16) float part[5][4][kHead];        // dr, dw, dk, da, db of each wave
-  __shared__ float res[6][kRun][kHead];                    // dr, dw, dk, dv, da, db
-  const int head = blockIdx.x % p.heads, s = blockIdx.x / p.heads;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__global__ void __launch_bounds__(kWalkThreads) time_mix_chains_kernel(TimeMixBack b, Chain to) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  ChunkLds& sh = *(ChunkLds*)lds;
+  const bool back = blockIdx.x & 1;
+  const int chain = blockIdx.x >> 1;
+  TimeMix p = b.f;
+  const int head = chain % p.heads, s = chain / p.heads;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int begin, end;
   seq_span(p.seq, s, begin, end);
+  const int chunks = (end - begin + kChunk - 1) / kChunk;
+  clear_counts(sh);
+  if (wave >= 4) {
+    if (back) {
+      p.v = b.dy;
+      prepare_chunks<T, true>(p, begin, end, sh, head, wave - 4, lane);
+    } else {
+      prepare_chunks<T, false>(p, begin, end, sh, head, wave - 4, lane);
+    }
+    return;
+  }
+  const int q = lane & 15, g = lane >> 4;
   const size_t state = ((size_t)s * p.heads + head) * kState;
-  const int row = wave * 16 + lane / 16, col = lane % 16 * 4;
-  const int runs = (end - begin + kRun - 1) / kRun;
-  // states before each run: begin / 16 + s is at most the runs of all
-  // sequences before this one
-  float* before = p.parts + ((size_t)(begin / kRun + s) * p.heads + head) * kState;
-  const size_t run_stride = (size_t)p.heads * kState;
-  // states before each token of the run at hand
-  float* within = p.parts + ((size_t)(p.seq.tokens / kRun + p.seq.nseq) * p.heads + (size_t)blockIdx.x * kRun) * kState;
-  const int mine = row * kHead + col;
-
-  const void* src[7] = {p.r, p.w, p.k, p.v, p.a, p.b, b.dy};
-  auto stage = [&](int t0, int n) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 7 * n * 8; i += 256) {
-      const int which = i / (n * 8), t = i / 8 % n, c = i % 8 * 8;
-      float f[8];
-      load8<T>(src[which], (size_t)(t0 + t) * p.ld + head * kHead + c, f);
-      if (which == 1)
+  const size_t at = ((size_t)first_chunk(begin, s) * p.heads + head);
+  auto out = [](int, float4v) {};
+  auto rows = [&](float* base, int c, float4v u) {
+    float* to = base + (at + (size_t)c * p.heads) * (kChunk * kHead) + 4 * g * kHead + 16 * wave + q;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] = __builtin_amdgcn_exp2f(log2_decay(f[q]));
-      *(float4*)&in[which][t][c] = *(const float4*)f;
-      *(float4*)&in[which][t][c + 4] = *(const float4*)(f + 4);
-    }
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) to[i * kHead] = u[i];
   };
-  float4 S[4];
-  auto step = [&](int t) {
-    const float4 w = *(const float4*)&in[1][t][col], k = *(const float4*)&in[2][t][col];
-    const float4 a = *(const float4*)&in[4][t][col], bb = *(const float4*)&in[5][t][col];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float u = row_sum(dot4(S[j], a));
-      S[j] = axpy4(u, bb, axpy4(in[3][t][row + 4 * j], k, mul4(S[j], w)));
-    }
-  };
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    S[j] = p.state_in ? *(const float4*)(p.state_in + state + mine + 4 * j * kHead) : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < runs; ++c) {
-    const int t0 = begin + c * kRun, n = min(kRun, end - t0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *(float4*)(before + c * run_stride + mine + 4 * j * kHead) = S[j];
-    if (c + 1 == runs) break;
-    stage(t0, n);
-    for (int t = 0; t < n; ++t) step(t);
+  ChunkState st;
+  if (!back) {
+    st.load(p.state_in ? p.state_in + state : nullptr, wave, lane);
+    walk_chunks<T, 1, false, false>(
+        &st, chunks, sh, wave, lane, [&](int c) { st.store(to.S + (at + (size_t)c * p.heads) * kState, wave, lane); },
+        [&](int c, float4v u) { rows(to.U, c, u); }, out);
+  } else {
+    st.load(b.dstate_out ? b.dstate_out + state : nullptr, wave, lane);
+    walk_chunks<T, 1, false, true>(
+        &st, chunks, sh, wave, lane,
+        [&](int c) { st.store(to.D + (at + (size_t)(chunks - 1 - c) * p.heads) * kState, wave, lane); },
+        [&](int c, float4v u) { rows(to.Z, chunks - 1 - c, u); }, out);
+    if (b.dstate_in) st.store(b.dstate_in + state, wave, lane);
   }
-  float4 D[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    D[j] = b.dstate_out ? *(const float4*)(b.dstate_out + state + mine + 4 * j * kHead) : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = runs - 1; c >= 0; --c) {
-    const int t0 = begin + c * kRun, n = min(kRun, end - t0);
-    stage(t0, n);
-    // each lane stores and loads its own elements only
-#pragma unroll
-    for (int j = 0; j < 4; ++j) S[j] = *(const float4*)(before + c * run_stride + mine + 4 * j * kHead);
-    for (int t = 0; t < n; ++t) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *(float4*)(within + t * kState + mine + 4 * j * kHead) = S[j];
-      step(t);
-    }
-    for (int t = n - 1; t >= 0; --t) {
-      const float4 r = *(const float4*)&in[0][t][col], w = *(const float4*)&in[1][t][col];
-      const float4 k = *(const float4*)&in[2][t][col], a = *(const float4*)&in[4][t][col];
-      const float4 bb = *(const float4*)&in[5][t][col];
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-      float4 dr = zero, dw = zero, dk = zero, da = zero, db = zero;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float dy = in[6][t][row + 4 * j], v = in[3][t][row + 4 * j];
-        dr = axpy4(dy, S[j], dr);
-        D[j] = axpy4(dy, r, D[j]);
-        S[j] = *(const float4*)(within + t * kState + mine + 4 * j * kHead);  // the state before
-        const float u = row_sum(dot4(S[j], a));
-        const float du = row_sum(dot4(D[j], bb)), dv = row_sum(dot4(D[j], k));
-        dk = axpy4(v, D[j], dk);
-        db = axpy4(u, D[j], db);
-        da = axpy4(du, S[j], da);
-        const float4 ds = mul4(D[j], S[j]);
-        dw = make_float4(dw.x + ds.x, dw.y + ds.y, dw.z + ds.z, dw.w + ds.w);
-        D[j] = axpy4(du, a, mul4(D[j], w));
-        if (lane % 16 == 0) res[3][t][row + 4 * j] = dv;
-      }
-      float4 all[5] = {dr, dw, dk, da, db};
-#pragma unroll
-      for (int q = 0; q < 5; ++q) {
-        const float4 v = cols_sum(all[q]);
-        if (lane < 16) *(float4*)&part[q][wave][col] = v;
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 5 * kHead; i += 256) {
-        const int q = i / kHead, c2 = i % kHead;
-        const float v = ((part[q][0][c2] + part[q][1][c2]) + part[q][2][c2]) + part[q][3][c2];
-        res[q < 3 ? q : q + 1][t][c2] = v;
-      }
-      __syncthreads();
-    }
-    void* dst[6] = {b.dr, b.dw, b.dk, b.dv, b.da, b.db};
-    for (int i = threadIdx.x; i < 6 * n * 8; i += 256) {
-      const int which = i / (n * 8), t = i / 8 % n, c2 = i % 8 * 8;
-      float f[8];
-      const size_t at = (size_t)(t0 + t) * p.ld + head * kHead + c2;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = res[which][t][c2 + q];
-      if (which == 1) {
-        float raw[8];
-        load8<T>(p.w, at, raw);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float sg = sigmoid_f32(raw[q]);
-          f[q] *= in[1][t][c2 + q] * -kDecay * sg * (1.f - sg);
-        }
-      }
-      store8<T>(dst[which], at, f);
-    }
-  }
-  if (b.dstate_in)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *(float4*)(b.dstate_in + state + mine + 4 * j * kHead) = D[j];
 }
+
+namespace {
+constexpr int kPad = 68;  // floats of a row of decays: 16-byte writes of 16 rows spread over the banks
+
+// Operands of a chunk's gradients: rows [16][64] in blocks of eight channels
+// (row_block), two bf16 terms, and the 16x16 matrices as operands.
+struct GradLds {
+  uint4 a[2][128], r[2][128], b[2][128], k[2][128], u[2][128], z[2][128], dy[2][128], v[2][128];
+  float fall[kChunk][kPad], sig[kChunk][kPad];
+  float diag[2][kChunk];  // of dQb and dQk, which are without it below
+  uint4 mr[2][64];  // (dQb, dQk), two terms
+  uint4 ma[2][64];  // (dAb, dAk)
+  uint4 mb[2][64];  // (dQb^T, dAb^T)
+  uint4 mk[2][64];  // (dQk^T, dAk^T)
+  uint4 mv[2][64];  // (Qk^T, Ak^T)
+};
+
+template <int NA, int NB>
+__device__ __forceinline__ float4v mul_terms(const uint4* a, const uint4* b, float4v c) {
+  if (NB > 1) c = mfma32(a[0], b[NB - 1], c);
+  if (NA > 1) c = mfma32(a[NA - 1], b[0], c);
+  return mfma32(a[0], b[0], c);
+}
+
+// X Y^T over the 64 channels of two rows' worth of operands in LDS: row 4 g + i
+// of X, row q of Y.
+template <int NA, int NB>
+__device__ __forceinline__ float4v gram_rows(const uint4 (*x)[128], const uint4 (*y)[128], int q, int g) {
+  float4v c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = row_block(q, 4 * h + g);
+    uint4 a[NA], b[NB];
+#pragma unroll
+    for (int n = 0; n < NA; ++n) a[n] = x[n][at];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) b[n] = y[n][at];
+    c = mul_terms<NA, NB>(a, b, c);
+  }
+  return c;
+}
+
+// Stores a 16x16 result (row 4 g + i, column q) as half `half` of an operand
+// whose row is q and whose slot is 4 g + i; entries with KEEP(slot - q) only.
+template <typename Keep>
+__device__ __forceinline__ void put_half(uint4 (*m)[64], int half, float4v x, int q, int g, int lane, Keep keep) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!keep(4 * g + i - q)) x[i] = 0.f;
+  uint2 t[2];
+  split4<2>(x, t);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) ((uint2*)&m[n][lane])[half] = t[n];
+}
+
+// Entry i of four rows of a two-term operand half (x, y words).
+__device__ __forceinline__ float entry(const uint4* t, int half, int i) {
+  float s = 0.f;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const uint32_t w = half ? (i < 2 ? t[n].z : t[n].w) : (i < 2 ? t[n].x : t[n].y);
+    s += BF16::up((i & 1) ? w >> 16 : w & 0xffffu);
+  }
+  return s;
+}
+}  // namespace
+
+// The gradients of one chunk and head: four waves, of which wave w takes
+// channels 16 w .. 16 w + 15.
+template <typename T>
+__global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Chain from) {
+  __shared__ __align__(16) GradLds sh;
+  const TimeMix& p = b.f;
+  constexpr int NV = ChunkHead<T>::kV;
+  const int head = blockIdx.x % p.heads, j = blockIdx.x / p.heads;
+  int begin, end, c;
+  if (!find_chunk(p.seq, j, begin, end, c)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int q = lane & 15, g = lane >> 4;
+  const int t0 = begin + c * kChunk, n = min(kChunk, end - t0);
+  const size_t at = (size_t)j * p.heads + head;
+
+  // S and D with this wave's columns of k, and D with its rows of v
+  float S[16], D[16], Dv[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const size_t e = at * kState + (32 * h + 8 * g + i) * kHead + 16 * wave + q;
+      S[8 * h + i] = from.S[e];
+      D[8 * h + i] = from.D[e];
+    }
+    load8f(from.D + at * kState + (16 * wave + q) * kHead + 32 * h + 8 * g, Dv + 8 * h);
+  }
+
+  // rows: token q, channels 16 w + 4 g .. + 3
+  {
+    const bool held = q < n;
+    const size_t e = (size_t)(t0 + q) * p.ld + head * kHead + 16 * wave + 4 * g;
+    const void* src[7] = {p.r, p.w, p.k, p.a, p.b, p.v, b.dy};
+    uint2 raw[7];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      const uint32_t other = i == 1 ? T::kMinusInf2 : 0u;
+      raw[i] = held ? *(const uint2*)((const uint16_t*)src[i] + e) : make_uint2(other, other);
+    }
+    const size_t er = at * (kChunk * kHead) + q * kHead + 16 * wave + 4 * g;
+    const float4v u = *(const float4v*)(from.U + er), z = *(const float4v*)(from.Z + er);
+    float x[4], fall[4], before[4], sig[4], grow[4];
+    auto up4 = [&](int i) {
+      up2<T>(raw[i].x, x);
+      up2<T>(raw[i].y, x + 2);
+    };
+    up4(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sig[i] = sigmoid_f32(x[i]);
+      float l = -(kDecay * kLog2e) * sig[i];
+      l += dpp<0x111>(l);
+      l += dpp<0x112>(l);
+      l += dpp<0x114>(l);
+      l += dpp<0x118>(l);
+      fall[i] = __builtin_amdgcn_exp2f(l);
+      grow[i] = __builtin_amdgcn_exp2f(-l);
+      before[i] = dpp_or<0x111>(1.f, fall[i]);
+    }
+    *(float4v*)&sh.fall[q][16 * wave + 4 * g] = float4v{fall[0], fall[1], fall[2], fall[3]};
+    *(float4v*)&sh.sig[q][16 * wave + 4 * g] = float4v{sig[0], sig[1], sig[2], sig[3]};
+    const int block = row_block(q, 2 * wave + (g >> 1)), half = g & 1;
+    auto put2 = [&](uint4(*m)[128], float4v f) {
+      uint2 t[2];
+      split4<2>(f, t);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ((uint2*)&m[i][block])[half] = t[i];
+    };
+    auto put_scaled = [&](uint4(*m)[128], int i, const float* s) {
+      up4(i);
+      put2(m, float4v{x[0] * s[0], x[1] * s[1], x[2] * s[2], x[3] * s[3]});
+    };
+    put_scaled(sh.r, 0, fall);
+    put_scaled(sh.k, 2, grow);
+    put_scaled(sh.a, 3, before);
+    put_scaled(sh.b, 4, grow);
+    put2(sh.u, u);
+    put2(sh.z, z);
+#pragma unroll
+    for (int i = 5; i < 7; ++i) {
+      uint4(*m)[128] = i == 5 ? sh.v : sh.dy;
+      if (NV == 1) {
+        ((uint2*)&m[0][block])[half] = raw[i];
+      } else {
+        up4(i);
+        put2(m, float4v{x[0], x[1], x[2], x[3]});
+      }
+    }
+  }
+  __syncthreads();
+
+  // the 16x16 matrices, both ways round
+  auto strict = [](int d) { return d < 0; };          // slot < row
+  auto upper = [](int d) { return d >= 0; };
+  auto strict_upper = [](int d) { return d > 0; };
+  auto put_diag = [&](float* to, float4v x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * g + i == q) to[q] = x[i];
+  };
+  if (wave == 0) {
+    const float4v x = gram_rows<2, NV>(sh.u, sh.dy, q, g);
+    put_diag(sh.diag[0], x);
+    put_half(sh.mr, 0, x, q, g, lane, strict);
+    put_half(sh.mb, 0, gram_rows<NV, 2>(sh.dy, sh.u, q, g), q, g, lane, strict_upper);
+  } else if (wave == 1) {
+    const float4v x = gram_rows<NV, NV>(sh.v, sh.dy, q, g);
+    put_diag(sh.diag[1], x);
+    put_half(sh.mr, 1, x, q, g, lane, strict);
+    put_half(sh.mk, 0, gram_rows<NV, NV>(sh.dy, sh.v, q, g), q, g, lane, strict_upper);
+    put_half(sh.mv, 0, gram_rows<2, 2>(sh.r, sh.k, q, g), q, g, lane, upper);
+  } else if (wave == 2) {
+    put_half(sh.ma, 0, gram_rows<2, 2>(sh.u, sh.z, q, g), q, g, lane, strict);
+    put_half(sh.mb, 1, gram_rows<2, 2>(sh.z, sh.u, q, g), q, g, lane, strict_upper);
+  } else {
+    put_half(sh.ma, 1, gram_rows<NV, 2>(sh.v, sh.z, q, g), q, g, lane, strict);
+    put_half(sh.mk, 1, gram_rows<2, NV>(sh.z, sh.v, q, g), q, g, lane, strict_upper);
+    put_half(sh.mv, 1, gram_rows<2, 2>(sh.a, sh.k, q, g), q, g, lane, strict_upper);
+  }
+  __syncthreads();
+
+  const float4v zero = {0.f, 0.f, 0.f, 0.f};
+  float4v dr = zero, da = zero, db = zero, dk = zero, dv = zero;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = row_block(q, 4 * h + g);
+    uint4 m[2], x[2];
+    auto rows = [&](const uint4(*from_)[128]) {
+      x[0] = from_[0][row];
+      x[1] = from_[1][row];
+    };
+    split8<2>(S + 8 * h, m);
+    rows(sh.dy);
+    dr = mul_terms<NV, 2>(x, m, dr);
+    rows(sh.z);
+    da = mul_terms<2, 2>(x, m, da);
+    split8<2>(D + 8 * h, m);
+    rows(sh.u);
+    db = mul_terms<2, 2>(x, m, db);
+    rows(sh.v);
+    dk = mul_terms<NV, 2>(x, m, dk);
+    split8<2>(Dv + 8 * h, m);
+    rows(sh.k);
+    dv = mul_terms<2, 2>(x, m, dv);
+  }
+  const int ch = 16 * wave + 4 * (q & 3);
+  uint4 bk[2], ra[2], yz[2], m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    bk[i] = pair(rows4(sh.b[i], g, q, ch), rows4(sh.k[i], g, q, ch));
+    ra[i] = pair(rows4(sh.r[i], g, q, ch), rows4(sh.a[i], g, q, ch));
+    yz[i] = pair(i < NV ? rows4(sh.dy[i], g, q, ch) : make_uint2(0, 0), rows4(sh.z[i], g, q, ch));
+  }
+  // sum_v D o S and the chunk's own part of it, before dB and dK get the rest
+  float last = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) last = fmaf(S[i], D[i], last);
+  float4v R, A, B, K;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    R[i] = entry(ra, 0, i);
+    A[i] = entry(ra, 1, i);
+    B[i] = entry(bk, 0, i);
+    K[i] = entry(bk, 1, i);
+    last = fmaf(B[i], db[i], fmaf(K[i], dk[i], last));
+  }
+  last += __shfl_xor(last, 16);
+  last += __shfl_xor(last, 32);
+  auto mats = [&](const uint4(*x)[64]) {
+    m[0] = x[0][lane];
+    m[1] = x[1][lane];
+  };
+  mats(sh.mr);
+  dr = mul_terms<2, 2>(m, bk, dr);
+  mats(sh.ma);
+  da = mul_terms<2, 2>(m, bk, da);
+  mats(sh.mb);
+  db = mul_terms<2, 2>(m, ra, db);
+  mats(sh.mk);
+  dk = mul_terms<2, 2>(m, ra, dk);
+  mats(sh.mv);
+  dv = mul_terms<2, 2>(m, yz, dv);
+
+  // decays: dL, then its sums from the end; lane (g, q) has tokens 4 g + i of
+  // channel 16 w + q
+  float4v dl = R * dr - B * db - K * dk;
+  const float4v next = A * da;
+  const float4v mb = *(const float4v*)&sh.diag[0][4 * g], mk = *(const float4v*)&sh.diag[1][4 * g];
+  dr += mb * B + mk * K;
+  db += mb * R;
+  dk += mk * R;
+  const float up = __shfl_down(next[0], 16);
+  dl[0] += next[1];
+  dl[1] += next[2];
+  dl[2] += next[3];
+  dl[3] += g == 3 ? last : up;
+  dl[2] += dl[3];
+  dl[1] += dl[2];
+  dl[0] += dl[1];
+  const float all = dl[0];
+  float after = 0.f;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    const float x = __shfl_down(all, 16 * i);
+    if (g + i < 4) after += x;
+  }
+  float4v dw;
+  {
+    const float* fall = &sh.fall[4 * g][16 * wave + q];
+    const float* sig = &sh.sig[4 * g][16 * wave + q];
+    float f = g ? fall[-kPad] : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = sig[i * kPad];
+      dw[i] = (dl[i] + after) * (-kDecay * s * (1.f - s));
+      da[i] *= f;
+      f = fall[i * kPad];
+      dr[i] *= f;
+      f = fall[i * kPad];
+      const float grow = __builtin_amdgcn_rcpf(f);
+      db[i] *= grow;
+      dk[i] *= grow;
+    }
+  }
+  // through LDS to whole rows; the row operands are done with
+  __syncthreads();
+  uint16_t* out = (uint16_t*)&sh.a[0][0];  // [6][16][64]
+  static_assert(sizeof(sh.a) + sizeof(sh.r) + sizeof(sh.b) >= 6 * kChunk * kHead * 2, "outputs fit");
+  const float4v all6[6] = {dr, dw, dk, dv, da, db};
+#pragma unroll
+  for (int o = 0; o < 6; ++o)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      out[(o * kChunk + 4 * g + i) * kHead + 16 * wave + q] = (uint16_t)T::down2(all6[o][i], 0.f);
+  __syncthreads();
+  void* dst[6] = {b.dr, b.dw, b.dk, b.dv, b.da, b.db};
+#pragma unroll
+  for (int o = 0; o < 6; o += 2) {
+    const int which = o + (threadIdx.x >> 7), t = (threadIdx.x >> 3) & 15, c8 = threadIdx.x & 7;
+    if (t < n)
+      *(uint4*)((uint16_t*)(threadIdx.x >> 7 ? dst[o + 1] : dst[o]) + (size_t)(t0 + t) * p.ld + head * kHead + 8 * c8) =
+          *(const uint4*)(out + (which * kChunk + t) * kHead + 8 * c8);
+  }
+}
+
+namespace {
+size_t chunk_slots(int64_t tokens, int64_t nseq) { return (size_t)(tokens / kChunk + nseq); }
+}  // namespace
 
 size_t time_mix_back_bytes(int64_t tokens, int64_t heads, int64_t nseq) {
-  return ((size_t)(tokens / kRun + nseq) + (size_t)nseq * kRun) * heads * kState * 4;
+  return chunk_slots(tokens, nseq) * heads * (2 * kState + 2 * kChunk * kHead) * 4;
 }
 
-hipError_t launch_time_mix_back(const TimeMixBack& b, bool bf16, hipStream_t st) {
-  const dim3 grid((unsigned)b.f.seq.nseq * b.f.heads), block(256);
-  if (bf16)
-    hipLaunchKernelGGL(time_mix_back_kernel<BF16>, grid, block, 0, st, b);
-  else
-    hipLaunchKernelGGL(time_mix_back_kernel<F16>, grid, block, 0, st, b);
+namespace {
+template <typename T>
+hipError_t start_back(const TimeMixBack& b, hipStream_t st) {
+  static const hipError_t attr = allow_lds(time_mix_chains_kernel<T>);
+  if (attr != hipSuccess) return attr;
+  const size_t n = chunk_slots(b.f.seq.tokens, b.f.seq.nseq) * b.f.heads;
+  Chain c;
+  c.S = b.f.parts;
+  c.D = c.S + n * kState;
+  c.U = c.D + n * kState;
+  c.Z = c.U + n * kChunk * kHead;
+  hipLaunchKernelGGL(time_mix_chains_kernel<T>, dim3(2u * b.f.seq.nseq * b.f.heads), dim3(kWalkThreads), sizeof(ChunkLds), st, b,
+                     c);
+  if (b.f.seq.tokens > 0)
+    hipLaunchKernelGGL(time_mix_grad_kernel<T>, dim3((unsigned)n), dim3(256), 0, st, b, c);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_time_mix_back(const TimeMixBack& b, bool bf16, hipStream_t st) {
+  return bf16 ? start_back<BF16>(b, st) : start_back<F16>(b, st);
 }
 
 }  // namespace rq

@@ -118,7 +118,7 @@ __device__ __forceinline__ float4v mul_values(const uint2* a, const uint2* b, fl
 // hold the state.
 struct ChunkOps {
   uint4 a[3][2][64];    // A: terms, channel halves, lanes (row q, channels 32 h + 8 g + j)
-  uint4 r[2][2][64];    // R, two terms
+  uint4 r[2][2][64];    // R, two terms (forward only, as q)
   uint4 q[2][64];       // row q, slots j < 4: Qb at 4 g + j, j >= 4: Qk
   uint2 t[3][64];       // T: row q, slots 4 g + i
   uint2 ak[3][64];      // Ak: row q, slots 4 g + i
@@ -157,11 +157,18 @@ __device__ __forceinline__ float dpp_or(float old, float v) {
 // owns it; lane 16 g + q has token q and channels 32 h + 8 g + 0..7.  Places
 // past the sequence's end are neutral: a raw decay of -inf, which is a decay
 // of 1, and zeros everywhere else.
-template <typename T>
+//
+// REV: the operands of the gradient's walk back.  With D the gradient of the
+// state after the chunk times exp L_15,
+//   Z = T^T (B D^T + Qb^T dY),   dS = D + Z^T A + dY^T R
+// which is the forward chain with B for A, Qb^T for Ak, T^T for T, A and R for
+// B and K, and dY for V (p.v is dY then, and p.k is not read).
+template <typename T, bool REV = false>
 struct ChunkPrep {
+  static constexpr int kR = REV ? 3 : 2;  // terms of R
   uint4 raw[6][2];  // r, w, k, v, a, b
   float fall[16], grow[16], before[16];
-  uint4 at[3][2], rt[2][2], bt[3][2], kt[3][2];
+  uint4 at[3][2], rt[kR][2], bt[3][2], kt[3][2];
   float4v ab, ak, qb, qk;
 
   __device__ __forceinline__ void load(const TimeMix& p, int head, int t0, int n, int lane) {
@@ -172,7 +179,8 @@ struct ChunkPrep {
 #pragma unroll
     for (int i = 0; i < 6; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) raw[i][h] = block_or(i == 1 ? T::kMinusInf2 : 0u, src[i], at0 + 32 * h, held);
+      for (int h = 0; h < 2; ++h)
+        if (!REV || i != 2) raw[i][h] = block_or(i == 1 ? T::kMinusInf2 : 0u, src[i], at0 + 32 * h, held);
   }
 
   __device__ __forceinline__ static void up8(uint4 v, float* f) {
@@ -217,12 +225,15 @@ struct ChunkPrep {
       scaled(5, grow);
       split8<3>(x, t);
       bt[0][h] = t[0]; bt[1][h] = t[1]; bt[2][h] = t[2];
-      scaled(2, grow);
-      split8<3>(x, t);
-      kt[0][h] = t[0]; kt[1][h] = t[1]; kt[2][h] = t[2];
+      if (!REV) {
+        scaled(2, grow);
+        split8<3>(x, t);
+        kt[0][h] = t[0]; kt[1][h] = t[1]; kt[2][h] = t[2];
+      }
       scaled(0, fall);
-      split8<2>(x, t);
-      rt[0][h] = t[0]; rt[1][h] = t[1];
+      split8<kR>(x, t);
+#pragma unroll
+      for (int n = 0; n < kR; ++n) rt[n][h] = t[n];
     }
   }
 
@@ -245,6 +256,10 @@ struct ChunkPrep {
 
   __device__ __forceinline__ void grams() {
     ab = gram<3>(at, bt);  // row t = 4 g + i, column s = q
+    if (REV) {
+      ak = gram<3>(rt, bt);  // row t = 4 g + i, column s = q: the operand of Qb^T
+      return;
+    }
     ak = gram<3>(kt, at);  // row s = 4 g + i, column t = q: already the operand of Ak
     qb = gram<2>(bt, rt);
     qk = gram<2>(kt, rt);
@@ -257,12 +272,14 @@ struct ChunkPrep {
       const int block = row_block(q, 4 * h + g);
 #pragma unroll
       for (int n = 0; n < 3; ++n) {
-        o.a[n][h][lane] = at[n][h];
-        o.b[n][block] = bt[n][h];
-        o.k[n][block] = kt[n][h];
+        o.a[n][h][lane] = REV ? bt[n][h] : at[n][h];
+        o.b[n][block] = REV ? at[n][h] : bt[n][h];
+        o.k[n][block] = REV ? rt[n < kR ? n : 0][h] : kt[n][h];
       }
-      o.r[0][h][lane] = rt[0][h];
-      o.r[1][h][lane] = rt[1][h];
+      if (!REV) {
+        o.r[0][h][lane] = rt[0][h];
+        o.r[1][h][lane] = rt[1][h];
+      }
       put_v(o, block, raw[3][h], (T*)nullptr);
       if (q == 15)
 #pragma unroll
@@ -295,17 +312,28 @@ struct ChunkPrep {
   }
 
   // T = (1 - Ab)^-1 from T = 1 + T Ab: lane q has row q, and column s follows
-  // from the columns to its right.  Substitution, because the powers of Ab
-  // grow and cancel where neighbouring tokens share a direction.
+  // from the columns to its right (REV: T = 1 + Ab T, lane q has column q, and
+  // row s follows from the rows above).  Substitution, because the powers of
+  // Ab grow and cancel where neighbouring tokens share a direction.
   __device__ __forceinline__ void solve(ChunkOps& o, int lane) const {
     const int q = lane & 15, g = lane >> 4;
     float row[16];
+    if (REV) {
 #pragma unroll
-    for (int s = 15; s >= 0; --s) {
-      float x = q == s ? 1.f : 0.f;
+      for (int s = 0; s < 16; ++s) {
+        float x = q == s ? 1.f : 0.f;
 #pragma unroll
-      for (int u = 15; u > s; --u) x = fmaf(row[u], lane_of(ab[u & 3], 16 * (u >> 2) + s), x);
-      row[s] = x;
+        for (int u = 0; u < s; ++u) x = fmaf(row[u], lane_of(ab[s & 3], 16 * (s >> 2) + u), x);
+        row[s] = x;
+      }
+    } else {
+#pragma unroll
+      for (int s = 15; s >= 0; --s) {
+        float x = q == s ? 1.f : 0.f;
+#pragma unroll
+        for (int u = 15; u > s; --u) x = fmaf(row[u], lane_of(ab[u & 3], 16 * (u >> 2) + s), x);
+        row[s] = x;
+      }
     }
     uint2 t[3];
     split4<3>(pick4(row, g), t);
@@ -316,12 +344,13 @@ struct ChunkPrep {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int s = 4 * g + i;
-      if (s >= q) k[i] = 0.f;
+      if (REV ? s < q : s >= q) k[i] = 0.f;
       if (s > q) qbm[i] = qkm[i] = 0.f;
     }
     split4<3>(k, t);
 #pragma unroll
     for (int n = 0; n < 3; ++n) o.ak[n][lane] = t[n];
+    if (REV) return;
     uint2 b[2], c[2];
     split4<2>(qbm, b);
     split4<2>(qkm, c);
@@ -400,15 +429,18 @@ struct ChunkHead {
 };
 
 // Takes NS states over a chunk: the first with V, the second, if there is one,
-// without (the map alone).  OUT: Y of the first (row t = 4 g + i, column v = q).
+// without (the map alone).  OUT: Y of the first (row t = 4 g + i, column
+// v = q).  REV: back over it; the caller has multiplied the state by `end`.
+// save(U) takes U, or Z, as Y is laid out.
 //
 // What bounds it: the four waves' reads of the operands, 26 KB each, take the
 // LDS about as long as the products take the matrix units.  So they are
 // fetched ahead by hand, each stage's under the stage before: R and Q while
 // the state is cut into terms, B and K while U is made, and the next chunk's
 // A, Ak, V and T (`next`) under the state's update.
-template <typename T, int NS, bool OUT, typename Next>
-__device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o, ChunkHead<T>& hd, int lane, Next next) {
+template <typename T, int NS, bool OUT, bool REV, typename Next, typename Save>
+__device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o, ChunkHead<T>& hd, int lane, Next next,
+                                              Save save) {
   const int q = lane & 15, g = lane >> 4;
   constexpr int NV = ChunkHead<T>::kV;
   const float4v zero = {0.f, 0.f, 0.f, 0.f};
@@ -462,6 +494,7 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o,
     u[m] = mul_tokens(hd.t, s[m], zero);
     split4<3>(u[m], s[m]);
   }
+  save(u[0]);
   // S' = (S + U^T B + V^T K) diag(end), Y = R S^T + Q (U, V)
   uint4 uv[NS][3];
 #pragma unroll
@@ -474,15 +507,110 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o,
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const float4v end = *(const float4v*)&o.end[ChunkState::channel(n, g)];
+    const float4v end = REV ? float4v{1.f, 1.f, 1.f, 1.f} : *(const float4v*)&o.end[ChunkState::channel(n, g)];
     uint4 c[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) c[j] = pair(b[n][j], k[n][j]);
 #pragma unroll
-    for (int m = 0; m < NS; ++m) st[m].X[n] = mul32<3>(c, uv[m], st[m].X[n]) * end;
+    for (int m = 0; m < NS; ++m) {
+      st[m].X[n] = mul32<3>(c, uv[m], st[m].X[n]);
+      if (!REV) st[m].X[n] *= end;
+    }
   }
   if (OUT) y = mul32<2>(qq, uv[0], y);
   return y;
+}
+
+// A workgroup that walks a run of chunks: waves 0-3 hold the state, sixteen
+// channels of v each, and take it from chunk to chunk; the waves after them
+// prepare the chunks' operands ahead of them, in turn, in LDS buffers.  Two
+// counters per buffer order them: `ready` chunks written, and `done` four per
+// chunk read.  Every wait is for a count that the other side reaches by
+// itself: a buffer's chunk c waits for the readers of chunk c - kBuffers, who
+// wait for nothing later than it.
+constexpr int kBuffers = 4;
+constexpr int kPreps = 8;
+constexpr int kWalkThreads = 64 * (4 + kPreps);
+
+struct ChunkLds {
+  ChunkOps ops[kBuffers];
+  int ready[kBuffers], done[kBuffers];
+};
+
+__device__ __forceinline__ void clear_counts(ChunkLds& sh) {
+  if (threadIdx.x < kBuffers) sh.ready[threadIdx.x] = sh.done[threadIdx.x] = 0;
+  __syncthreads();
+}
+__device__ __forceinline__ int count_of(int* count) {
+  return __builtin_amdgcn_readfirstlane(__hip_atomic_load(count, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP));
+}
+__device__ __forceinline__ void wait_for(int* count, int want) {
+  while (count_of(count) < want) __builtin_amdgcn_s_sleep(1);
+}
+__device__ __forceinline__ void signal(int* count, int lane) {
+  if (lane == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// The side of preparing wave `mine`: the chunks of tokens begin..end, from the
+// last to the first with REV.
+template <typename T, bool REV>
+__device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int end, ChunkLds& sh, int head, int mine, int lane) {
+  const int chunks = (end - begin + kChunk - 1) / kChunk;
+  ChunkPrep<T, REV> prep;
+  for (int c = mine; c < chunks; c += kPreps) {
+    ChunkOps& o = sh.ops[c % kBuffers];
+    const int t = begin + (REV ? chunks - 1 - c : c) * kChunk;
+    prep.load(p, head, t, min(kChunk, end - t), lane);
+    prep.decays();
+    // without these the scheduler mixes the stages and needs more registers
+    __builtin_amdgcn_sched_barrier(0);
+    prep.factors();
+    __builtin_amdgcn_sched_barrier(0);
+    prep.grams();
+    __builtin_amdgcn_sched_barrier(0);
+    wait_for(&sh.done[c % kBuffers], c / kBuffers * 4);
+    prep.put_rows(o, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    prep.solve(o, lane);
+    signal(&sh.ready[c % kBuffers], lane);
+  }
+}
+
+// The state's waves' side: NS states (see chunk_step) over the run.  In the
+// c-th chunk of the walk: before(c) with the state at hand (multiplied by
+// `end` with REV), save(c, U or Z), and out(c, Y) with OUT.
+template <typename T, int NS, bool OUT, bool REV, typename Before, typename Save, typename Out>
+__device__ __forceinline__ void walk_chunks(ChunkState* st, int chunks, ChunkLds& sh, int wave, int lane, Before before,
+                                            Save save, Out out) {
+  ChunkHead<T> hd;
+  if (chunks > 0) {
+    wait_for(&sh.ready[0], 1);
+    hd.fetch(sh.ops[0], wave, lane);
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int n = c + 1;
+    const ChunkOps& o = sh.ops[c % kBuffers];
+    if (REV)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st[0].X[i] *= *(const float4v*)&o.end[ChunkState::channel(i, lane >> 4)];
+    before(c);
+    const float4v y = chunk_step<T, NS, OUT, REV>(
+        st, o, hd, lane,
+        [&] {
+          if (n < chunks) {
+            wait_for(&sh.ready[n % kBuffers], n / kBuffers + 1);
+            hd.fetch(sh.ops[n % kBuffers], wave, lane);
+          }
+        },
+        [&](float4v u) { save(c, u); });
+    signal(&sh.done[c % kBuffers], lane);
+    if (OUT) out(c, y);
+  }
+}
+
+template <typename K>
+hipError_t allow_lds(K* kernel) {
+  return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(ChunkLds));
 }
 
 }  // namespace rq

@@ -412,7 +412,7 @@ int rq_gemm_int8_acc(const int8_t *xq, int64_t m, const rq_qweight *w, int32_t *
  * Workspaces are as for the products; the split counters at their head are
  * neither read nor written.  None of these calls allocates or synchronizes,
  * and each gives the same bits for the same arguments.  nseq * heads and nseq
- * stay below 2^22, tokens * ld below 2^40.
+ * stay below 2^21, tokens * ld below 2^40.
  */
 
 /* The state recurrence, per head of 64 channels with a state S[64][64] (rows:
@@ -436,7 +436,7 @@ int rq_time_mix(int dtype, const void *r, const void *w, const void *k, const vo
  * [nseq][heads][64][64] without slots (NULL: zeros).  The workspace holds the
  * states along the sequences: at least rq_time_mix_backward_bytes(tokens,
  * heads, nseq) bytes (host-only; 0 for arguments out of range), else
- * RQ_ERR_WORKSPACE. */
+ * RQ_ERR_WORKSPACE.  (tokens / 16 + nseq) * heads stays below 2^24. */
 size_t rq_time_mix_backward_bytes(int64_t tokens, int64_t heads, int64_t nseq);
 int rq_time_mix_backward(int dtype, const void *r, const void *w, const void *k, const void *v, const void *a,
                          const void *b, int64_t tokens, int64_t heads, int64_t ld, const int32_t *cu, int64_t nseq,
