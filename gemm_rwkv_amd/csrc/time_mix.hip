@@ -106,6 +106,9 @@ struct SegmentSplit {
 };
 
 namespace {
+constexpr int kPreps = 8;     // preparing waves
+constexpr int kMapPreps = 4;  // with two states per wave, which take more registers
+
 struct Segment {
   int seq, begin, end;
   int nth, of;  // which of the sequence's segments
@@ -140,7 +143,7 @@ __device__ __forceinline__ bool find_segment(const Sequences& s, int len, int id
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(kWalkThreads) time_mix_chunk_kernel(TimeMix p, SegmentSplit split) {
+__global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chunk_kernel(TimeMix p, SegmentSplit split) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kWalkThreads) time_mix_chunk_kernel(TimeMix p,
   if (!find_segment(p.seq, split.len, idx, sg)) return;
   clear_counts(sh);
   if (wave >= 4) {
-    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
+    prepare_chunks<T, false, kPreps>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
     return;
   }
   const int slot = slot_of(p.slots, sg.seq);
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kWalkThreads) time_mix_chunk_kernel(TimeMix p,
 
 // G and P of a segment; of a first one the state after it, and before it.
 template <typename T>
-__global__ void __launch_bounds__(kWalkThreads) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
+__global__ void __launch_bounds__(walk_threads(kMapPreps)) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kWalkThreads) time_mix_segment_kernel(TimeMix 
   if (!find_segment(p.seq, split.len, idx, sg) || sg.nth + 1 == sg.of) return;
   clear_counts(sh);
   if (wave >= 4) {
-    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
+    prepare_chunks<T, false, kMapPreps>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
     return;
   }
   const int slot = slot_of(p.slots, sg.seq);
@@ -246,8 +249,8 @@ hipError_t start_chunks(const TimeMix& p, hipStream_t st) {
   SegmentSplit split = {segment_len(p), p.parts};
   const unsigned chains = (unsigned)(split.len ? p.seq.tokens / split.len + p.seq.nseq : p.seq.nseq) * p.heads;
   if (split.len)
-    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(kWalkThreads), sizeof(ChunkLds), st, p, split);
-  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(kWalkThreads), sizeof(ChunkLds), st, p, split);
+    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(walk_threads(kMapPreps)), sizeof(ChunkLds), st, p, split);
+  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(walk_threads(kPreps)), sizeof(ChunkLds), st, p, split);
   return hipGetLastError();
 }
 }  // namespace

@@ -25,6 +25,7 @@
 namespace rq {
 
 namespace {
+constexpr int kPreps = 8;  // preparing waves of a chain
 constexpr int kState = kHead * kHead;
 
 // Chunk c of sequence s is number begin / 16 + s + c of all chunks: at least
@@ -55,7 +56,7 @@ struct Chain {
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(kWalkThreads) time_mix_chains_kernel(TimeMixBack b, Chain to) {
+__global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chains_kernel(TimeMixBack b, Chain to) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const bool back = blockIdx.x & 1;
@@ -71,9 +72,9 @@ __global__ void __launch_bounds__(kWalkThreads) time_mix_chains_kernel(TimeMixBa
   if (wave >= 4) {
     if (back) {
       p.v = b.dy;
-      prepare_chunks<T, true>(p, begin, end, sh, head, wave - 4, lane);
+      prepare_chunks<T, true, kPreps>(p, begin, end, sh, head, wave - 4, lane);
     } else {
-      prepare_chunks<T, false>(p, begin, end, sh, head, wave - 4, lane);
+      prepare_chunks<T, false, kPreps>(p, begin, end, sh, head, wave - 4, lane);
     }
     return;
   }
@@ -174,7 +175,7 @@ template <typename T>
 __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Chain from) {
   __shared__ __align__(16) GradLds sh;
   const TimeMix& p = b.f;
-  constexpr int NV = ChunkHead<T>::kV;
+  constexpr int NV = ChunkHead<T, false>::kV;
   const int head = blockIdx.x % p.heads, j = blockIdx.x / p.heads;
   int begin, end, c;
   if (!find_chunk(p.seq, j, begin, end, c)) return;
@@ -432,7 +433,7 @@ hipError_t start_back(const TimeMixBack& b, hipStream_t st) {
   c.D = c.S + n * kState;
   c.U = c.D + n * kState;
   c.Z = c.U + n * kChunk * kHead;
-  hipLaunchKernelGGL(time_mix_chains_kernel<T>, dim3(2u * b.f.seq.nseq * b.f.heads), dim3(kWalkThreads), sizeof(ChunkLds), st, b,
+  hipLaunchKernelGGL(time_mix_chains_kernel<T>, dim3(2u * b.f.seq.nseq * b.f.heads), dim3(walk_threads(kPreps)), sizeof(ChunkLds), st, b,
                      c);
   if (b.f.seq.tokens > 0)
     hipLaunchKernelGGL(time_mix_grad_kernel<T>, dim3((unsigned)n), dim3(256), 0, st, b, c);

@@ -406,12 +406,14 @@ struct ChunkState {
   }
 };
 
-// The operands that a chunk starts with.
-template <typename T>
+// The operands that a chunk starts with; with REV also what scales the state
+// before it.
+template <typename T, bool REV>
 struct ChunkHead {
   static constexpr int kV = __is_same(T, BF16) ? 1 : 2;  // terms of V
   uint4 a[2][3];
   uint2 ak[3], v[kV], t[3];
+  float4v end[4];
 
   __device__ __forceinline__ void fetch(const ChunkOps& o, int wave, int lane) {
     const int q = lane & 15, g = lane >> 4;
@@ -425,24 +427,53 @@ struct ChunkHead {
     for (int n = 0; n < kV; ++n) v[n] = rows4(o.v[n], g, q, 16 * wave + 4 * (q & 3));
 #pragma unroll
     for (int n = 0; n < 3; ++n) t[n] = o.t[n][lane];
+    if (REV)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) end[n] = *(const float4v*)&o.end[ChunkState::channel(n, g)];
   }
 };
 
+// The state as operands of the next products: three terms.
+__device__ __forceinline__ void split_half(const ChunkState& st, int h, uint4* x) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = st.X[2 * h][i];
+    f[4 + i] = st.X[2 * h + 1][i];
+  }
+  split8<3>(f, x);
+}
+
+// Instruction mixes for the scheduler: N times one matrix instruction and then
+// so many of the others.
+template <int N, int READS, int VALU>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (READS) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+  }
+}
+
 // Takes NS states over a chunk: the first with V, the second, if there is one,
 // without (the map alone).  OUT: Y of the first (row t = 4 g + i, column
-// v = q).  REV: back over it; the caller has multiplied the state by `end`.
-// save(U) takes U, or Z, as Y is laid out.
+// v = q).  REV: back over it.  save(U) takes U, or Z, as Y is laid out.  x: the
+// states as operands, made again at the end; with REV the states are scaled by
+// the next chunk's `end` before that.
 //
-// What bounds it: the four waves' reads of the operands, 26 KB each, take the
-// LDS about as long as the products take the matrix units.  So they are
-// fetched ahead by hand, each stage's under the stage before: R and Q while
-// the state is cut into terms, B and K while U is made, and the next chunk's
-// A, Ak, V and T (`next`) under the state's update.
+// What bounds it: one wave's chain from state to state.  Its products are
+// about 800 cycles of the matrix unit; cutting results into terms and fetching
+// 26 KB of operands each take about as long, a fetch some 15 cycles of the
+// wave's issue and no more than fifteen in flight.  So the three are mixed by
+// hand, instruction by instruction: B, K and `end` between the products with A
+// and R, the next chunk's head (`next`) and the cutting of each half of the
+// new state between the products of its update.
 template <typename T, int NS, bool OUT, bool REV, typename Next, typename Save>
-__device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o, ChunkHead<T>& hd, int lane, Next next,
-                                              Save save) {
+__device__ __forceinline__ float4v chunk_step(ChunkState* st, uint4 (*x)[2][3], const ChunkOps& o, ChunkHead<T, REV>& hd,
+                                              int lane, Next next, Save save) {
   const int q = lane & 15, g = lane >> 4;
-  constexpr int NV = ChunkHead<T>::kV;
+  constexpr int NV = ChunkHead<T, REV>::kV;
   const float4v zero = {0.f, 0.f, 0.f, 0.f};
   uint4 r[2][2], qq[2];
   if (OUT) {
@@ -454,48 +485,39 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o,
     for (int n = 0; n < 2; ++n) qq[n] = o.q[n][lane];
   }
   __builtin_amdgcn_sched_barrier(0);
-  float4v u[NS], y = zero;
-#pragma unroll
-  for (int m = 0; m < NS; ++m) {
-    // U = T (A S^T + Ak V), and R S^T
-    uint4 x[2][3];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = st[m].X[2 * h][i];
-        f[4 + i] = st[m].X[2 * h + 1][i];
-      }
-      split8<3>(f, x[h]);
-    }
-    float4v u0 = mul32<3>(hd.a[0], x[0], zero), u1 = zero;
-    if (m == 0) u1 = mul_values<NV>(hd.ak, hd.v, u1);
-    u1 = mul32<3>(hd.a[1], x[1], u1);
-    u[m] = u0 + u1;
-    if (OUT && m == 0)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) y = mul32<2>(r[h], x[h], y);
-  }
-  __builtin_amdgcn_sched_barrier(0);
+  // A S^T + Ak V, R S^T
   uint2 b[4][3], k[4][3];
+  float4v end[4];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < 4; ++n) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       b[n][j] = rows4(o.b[j], g, q, ChunkState::channel(n, q & 3));
       k[n][j] = rows4(o.k[j], g, q, ChunkState::channel(n, q & 3));
     }
+    if (!REV) end[n] = *(const float4v*)&o.end[ChunkState::channel(n, g)];
+  }
+  float4v u0[NS], u1[NS], u[NS], y = zero;
+#pragma unroll
+  for (int m = 0; m < NS; ++m) {
+    u0[m] = mul32<3>(hd.a[0], x[m][0], zero);
+    u1[m] = mul32<3>(hd.a[1], x[m][1], zero);
+    if (m == 0) u1[m] = mul_values<NV>(hd.ak, hd.v, u1[m]);
+  }
+  if (OUT)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) y = mul32<2>(r[h], x[0][h], y);
+  interleave<(NS * 12 + NV + 1 + (OUT ? 6 : 0)), (OUT || NS == 2 ? 1 : 2), 0>();
   __builtin_amdgcn_sched_barrier(0);
   uint2 s[NS][3];
 #pragma unroll
   for (int m = 0; m < NS; ++m) {
+    u[m] = u0[m] + u1[m];
     split4<3>(u[m], s[m]);
     u[m] = mul_tokens(hd.t, s[m], zero);
     split4<3>(u[m], s[m]);
   }
   save(u[0]);
-  // S' = (S + U^T B + V^T K) diag(end), Y = R S^T + Q (U, V)
   uint4 uv[NS][3];
 #pragma unroll
   for (int n = 0; n < 3; ++n) {
@@ -504,20 +526,22 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o,
   }
   __builtin_amdgcn_sched_barrier(0);
   next();
-  __builtin_amdgcn_sched_barrier(0);
+  // S' = (S + U^T B + V^T K) diag(end), Y = R S^T + Q (U, V)
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const float4v end = REV ? float4v{1.f, 1.f, 1.f, 1.f} : *(const float4v*)&o.end[ChunkState::channel(n, g)];
     uint4 c[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) c[j] = pair(b[n][j], k[n][j]);
 #pragma unroll
-    for (int m = 0; m < NS; ++m) {
-      st[m].X[n] = mul32<3>(c, uv[m], st[m].X[n]);
-      if (!REV) st[m].X[n] *= end;
-    }
+    for (int m = 0; m < NS; ++m) st[m].X[n] = mul32<3>(c, uv[m], st[m].X[n]) * (REV ? hd.end[n] : end[n]);
+    if (n & 1)
+#pragma unroll
+      for (int m = 0; m < NS; ++m) split_half(st[m], n >> 1, x[m][n >> 1]);
   }
   if (OUT) y = mul32<2>(qq, uv[0], y);
+  interleave<12 * NS, 1, 0>();
+  interleave<(12 * NS + (OUT ? 3 : 0)), 0, 4>();
+  __builtin_amdgcn_sched_barrier(0);
   return y;
 }
 
@@ -529,8 +553,7 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, const ChunkOps& o,
 // itself: a buffer's chunk c waits for the readers of chunk c - kBuffers, who
 // wait for nothing later than it.
 constexpr int kBuffers = 4;
-constexpr int kPreps = 8;
-constexpr int kWalkThreads = 64 * (4 + kPreps);
+constexpr int walk_threads(int preps) { return 64 * (4 + preps); }
 
 struct ChunkLds {
   ChunkOps ops[kBuffers];
@@ -547,17 +570,22 @@ __device__ __forceinline__ int count_of(int* count) {
 __device__ __forceinline__ void wait_for(int* count, int want) {
   while (count_of(count) < want) __builtin_amdgcn_s_sleep(1);
 }
+// The LDS does a wave's operations in their order, so what the wave has read
+// or written before is done when the count changes; only the compiler has to
+// be kept from moving them.
 __device__ __forceinline__ void signal(int* count, int lane) {
-  if (lane == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+  asm volatile("" ::: "memory");
+  if (lane == 0) __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  asm volatile("" ::: "memory");
 }
 
 // The side of preparing wave `mine`: the chunks of tokens begin..end, from the
 // last to the first with REV.
-template <typename T, bool REV>
+template <typename T, bool REV, int PREPS>
 __device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int end, ChunkLds& sh, int head, int mine, int lane) {
   const int chunks = (end - begin + kChunk - 1) / kChunk;
   ChunkPrep<T, REV> prep;
-  for (int c = mine; c < chunks; c += kPreps) {
+  for (int c = mine; c < chunks; c += PREPS) {
     ChunkOps& o = sh.ops[c % kBuffers];
     const int t = begin + (REV ? chunks - 1 - c : c) * kChunk;
     prep.load(p, head, t, min(kChunk, end - t), lane);
@@ -582,25 +610,36 @@ __device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int 
 template <typename T, int NS, bool OUT, bool REV, typename Before, typename Save, typename Out>
 __device__ __forceinline__ void walk_chunks(ChunkState* st, int chunks, ChunkLds& sh, int wave, int lane, Before before,
                                             Save save, Out out) {
-  ChunkHead<T> hd;
+  ChunkHead<T, REV> hd;
+  uint4 x[NS][2][3];
   if (chunks > 0) {
     wait_for(&sh.ready[0], 1);
     hd.fetch(sh.ops[0], wave, lane);
+    if (REV)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) st[0].X[n] *= hd.end[n];
+#pragma unroll
+    for (int m = 0; m < NS; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) split_half(st[m], h, x[m][h]);
   }
   for (int c = 0; c < chunks; ++c) {
     const int n = c + 1;
     const ChunkOps& o = sh.ops[c % kBuffers];
-    if (REV)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) st[0].X[i] *= *(const float4v*)&o.end[ChunkState::channel(i, lane >> 4)];
     before(c);
+    // looked at early, so that the answer is here when it is needed
+    const int seen = __hip_atomic_load(&sh.ready[n % kBuffers], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     const float4v y = chunk_step<T, NS, OUT, REV>(
-        st, o, hd, lane,
+        st, x, o, hd, lane,
         [&] {
-          if (n < chunks) {
-            wait_for(&sh.ready[n % kBuffers], n / kBuffers + 1);
-            hd.fetch(sh.ops[n % kBuffers], wave, lane);
-          }
+          const int want = n < chunks ? n / kBuffers + 1 : 0;
+          if (__builtin_amdgcn_readfirstlane(seen) < want) wait_for(&sh.ready[n % kBuffers], want);
+          asm volatile("" ::: "memory");
+          // (past the last chunk whatever the buffer holds, for nothing)
+          hd.fetch(sh.ops[n % kBuffers], wave, lane);
+          if (REV && n >= chunks)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hd.end[i] = float4v{1.f, 1.f, 1.f, 1.f};
         },
         [&](float4v u) { save(c, u); });
     signal(&sh.done[c % kBuffers], lane);
