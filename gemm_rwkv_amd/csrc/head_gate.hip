@@ -160,25 +160,54 @@ __global__ void __launch_bounds__(256) head_gate_back_kernel(HeadGateBack b, int
   }
 }
 
-// Sums `count` rows of partial sums: 64 columns per workgroup, sixteen groups
-// of rows side by side, added in a fixed order.
-__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ parts, int count, int n, size_t stride,
-                                                         float* __restrict__ out) {
-  __shared__ float red[16][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), grp = threadIdx.x >> 6;
-  float s = 0.f;
-  if (col < n)
-    for (int i = grp; i < count; i += 16) s += parts[(size_t)i * stride + col];
-  red[grp][threadIdx.x & 63] = s;
+// Sums `count` rows of partial sums into up to three outputs, one after the
+// other in a row.  64 columns per workgroup, four per thread; 64 groups of
+// rows side by side, so that eight rows in flight per thread are all there is
+// to wait for; added in a fixed order.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ parts, int count, int n, SumTargets to) {
+  __shared__ float4v red[64][17];
+  const int c4 = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int col = blockIdx.x * 64 + 4 * c4;
+  float4v s = {0.f, 0.f, 0.f, 0.f};
+  if (col < n) {
+    const float* at = parts + col;
+    int i = grp;
+    for (; i + 7 * 64 < count; i += 8 * 64) {
+      float4v v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = *(const float4v*)(at + (size_t)(i + 64 * k) * n);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; i < count; i += 64) s += *(const float4v*)(at + (size_t)i * n);
+  }
+  red[grp][c4] = s;
   __syncthreads();
-  if (grp == 0 && col < n) {
-    for (int i = 1; i < 16; ++i) s += red[i][threadIdx.x];
-    out[col] = s;
+  if (threadIdx.x < 256) {
+    // four threads per four columns, sixteen groups each
+    const int part = threadIdx.x >> 6, e = threadIdx.x & 63;
+    float t = 0.f;
+    for (int k = 0; k < 16; ++k) t += red[16 * part + k][e >> 2][e & 3];
+    red[16 * part][e >> 2][e & 3] = t;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < n) {
+    const int e = threadIdx.x;
+    const float t = ((red[0][e >> 2][e & 3] + red[16][e >> 2][e & 3]) + red[32][e >> 2][e & 3]) + red[48][e >> 2][e & 3];
+    int c = blockIdx.x * 64 + e;
+    if (c < to.n[0]) {
+      to.out[0][c] = t;
+    } else if ((c -= to.n[0]) < to.n[1]) {
+      to.out[1][c] = t;
+    } else {
+      to.out[2][c - to.n[1]] = t;
+    }
   }
 }
 
-hipError_t launch_sum_parts(const float* parts, int count, int n, size_t stride, float* out, hipStream_t st) {
-  hipLaunchKernelGGL(sum_parts_kernel, dim3((n + 63) / 64), dim3(1024), 0, st, parts, count, n, stride, out);
+hipError_t launch_sum_parts(const float* parts, int count, const SumTargets& to, hipStream_t st) {
+  const int n = to.n[0] + to.n[1] + to.n[2];
+  hipLaunchKernelGGL(sum_parts_kernel, dim3((n + 63) / 64), dim3(1024), 0, st, parts, count, n, to);
   return hipGetLastError();
 }
 
@@ -203,10 +232,7 @@ hipError_t launch_head_gate_back(const HeadGateBack& b, bool bf16, hipStream_t s
     hipLaunchKernelGGL(head_gate_back_kernel<F16>, grid, dim3(256), 0, st, b, rows);
   hipError_t e = hipGetLastError();
   if (groups == 1 || e != hipSuccess) return e;
-  float* outs[3] = {b.dgamma, b.dbeta, b.du};
-  for (int i = 0; i < 3 && e == hipSuccess; ++i)
-    e = launch_sum_parts(b.parts + (size_t)i * width, (int)groups, width, 3 * (size_t)width, outs[i], st);
-  return e;
+  return launch_sum_parts(b.parts, (int)groups, {{b.dgamma, b.dbeta, b.du}, {width, width, width}}, st);
 }
 
 }  // namespace rq

@@ -75,9 +75,13 @@ struct ShiftNormBack {
 };
 hipError_t launch_shift_norm_back(const ShiftNormBack& p, bool bf16, hipStream_t st);
 
-// Sums rows 0..count-1 of parts (stride floats apart) over n columns into
-// out[n], in a fixed order (head_gate.hip).
-hipError_t launch_sum_parts(const float* parts, int count, int n, size_t stride, float* out, hipStream_t st);
+// Sums rows 0..count-1 of parts, [count][n0 + n1 + n2], into three arrays of
+// n0, n1 and n2 (multiples of four), in a fixed order (head_gate.hip).
+struct SumTargets {
+  float* out[3];
+  int n[3];
+};
+hipError_t launch_sum_parts(const float* parts, int count, const SumTargets& to, hipStream_t st);
 
 // ---- head norm, bonus and gate (head_gate.hip) ------------------------------
 struct HeadGate {

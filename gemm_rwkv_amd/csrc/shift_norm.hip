@@ -9,7 +9,7 @@
 // the next (shift_out).  One pass: two rows in, 1 + nmix out.  Bound by memory.
 //
 // A workgroup owns a run of consecutive rows and holds a row in registers,
-// eight channels per thread and vector; h of the row before stays in registers
+// several channels per thread; h of the row before stays in registers
 // from one row to the next and is computed again where a run begins inside a
 // sequence.
 #include "mix.h"
@@ -18,51 +18,77 @@ namespace rq {
 
 namespace {
 
-// Sums of two values over the workgroup, in a fixed order.  buf alternates
+// Sums of N values over the workgroup, in a fixed order.  buf alternates
 // between calls, so one barrier per call is enough.
-__device__ __forceinline__ void block_sum2(float& a, float& b, float2 (*red)[16], int& buf, int waves) {
-  a = wave_sum(a);
-  b = wave_sum(b);
-  if ((threadIdx.x & 63) == 0) red[buf][threadIdx.x >> 6] = make_float2(a, b);
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[16][4], int& buf, int waves) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[buf][threadIdx.x >> 6][k] = v[k];
   __syncthreads();
-  float sa = 0.f, sb = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 0.f;
   for (int i = 0; i < waves; ++i) {
-    const float2 v = red[buf][i];
-    sa += v.x;
-    sb += v.y;
+    const float4v x = *(const float4v*)red[buf][i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += x[k];
   }
-  a = sa;
-  b = sb;
   buf ^= 1;
 }
 
-// mean and 1 / sqrt(var + eps) of a row held in registers, in two passes
-template <int NV>
-__device__ __forceinline__ void row_stats(const float (*x)[8], const bool* on, int width, float eps, float2 (*red)[16],
-                                          int& buf, int waves, float& mean, float& rstd) {
-  float s = 0.f, z = 0.f;
+// A thread's share of a row's sum, and of its squares about the mean.
+template <int NV, int CH>
+__device__ __forceinline__ float part_sum(const float (*x)[CH], const bool* on) {
+  float s = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if (on[j])
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += x[j][i];
-  block_sum2(s, z, red, buf, waves);
-  mean = s / (float)width;
-  float q = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (on[j])
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(x[j][i] - mean, x[j][i] - mean, q);
-  block_sum2(q, z, red, buf, waves);
-  rstd = rsqrtf(q / (float)width + eps);
+      for (int i = 0; i < CH; ++i) s += x[j][i];
+  return s;
 }
+template <int NV, int CH>
+__device__ __forceinline__ float part_squares(const float (*x)[CH], const bool* on, float mean) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (on[j])
+#pragma unroll
+      for (int i = 0; i < CH; ++i) s = fmaf(x[j][i] - mean, x[j][i] - mean, s);
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void up8(uint4 v, float* f) {
+  up2<T>(v.x, f);
+  up2<T>(v.y, f + 2);
+  up2<T>(v.z, f + 4);
+  up2<T>(v.w, f + 6);
+}
+template <typename T>
+__device__ __forceinline__ void up4(uint2 v, float* f) {
+  up2<T>(v.x, f);
+  up2<T>(v.y, f + 2);
+}
+__device__ __forceinline__ uint2 raw4(const void* base, size_t elem) { return *(const uint2*)((const uint16_t*)base + elem); }
+template <typename T>
+__device__ __forceinline__ void load4(const void* base, size_t elem, float* f) {
+  up4<T>(raw4(base, elem), f);
+}
+template <typename T>
+__device__ __forceinline__ void store4(void* base, size_t elem, const float* f) {
+  *(uint2*)((uint16_t*)base + elem) = make_uint2(T::down2(f[0], f[1]), T::down2(f[2], f[3]));
+}
+__device__ __forceinline__ void load4f(const float* p, float* f) { *(float4*)f = *(const float4*)p; }
+__device__ __forceinline__ uint4 raw8(const void* base, size_t elem) { return *(const uint4*)((const uint16_t*)base + elem); }
 
 }  // namespace
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(512) shift_norm_kernel(ShiftNorm p, int rows, int tiles) {
-  __shared__ float2 red[2][16];
+  __shared__ __align__(16) float red[2][16][4];
   int buf = 0;
   const int waves = blockDim.x >> 6;
   const int width = p.width;
@@ -94,82 +120,136 @@ __global__ void __launch_bounds__(512) shift_norm_kernel(ShiftNorm p, int rows, 
     load8f(p.beta + col[j], beta[j]);
   }
 
-  // x' of row t in registers
-  auto fetch = [&](int t, float (*x)[8]) {
+  uint4 rx[NV], rd[NV];
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const size_t at = (size_t)t * p.ld + col[j];
-      load8<T>(p.x, at, x[j]);
+      rx[j] = raw8(p.x, at);
+      if (p.delta) rd[j] = raw8(p.delta, at);
+    }
+  };
+  auto sum = [&](float (*x)[8]) {  // x' of the row fetched
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      up8<T>(rx[j], x[j]);
       if (p.delta) {
         float d[8];
-        load8<T>(p.delta, at, d);
+        up8<T>(rd[j], d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[j][i] = fmaf(p.alpha, d[i], x[j][i]);
       }
     }
   };
-  auto norm = [&](float (*x)[8]) {
-    float mean, rstd;
-    row_stats<NV>(x, on, width, p.eps, red, buf, waves, mean, rstd);
+  auto norm = [&](float (*x)[8], float mean, float rstd) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[j][i] = fmaf((x[j][i] - mean) * rstd, gamma[j][i], beta[j][i]);
   };
+  const float inv = 1.f / (float)width;
 
   const int t0 = blockIdx.x * rows, t1 = min(p.seq.tokens, t0 + rows);
   int s = seq_of(p.seq, t0), begin, end;
   seq_span(p.seq, s, begin, end);
-  float h[NV][8], prev[NV][8];
-  if (t0 > begin) {
-    fetch(t0 - 1, prev);
-    norm(prev);
-  }
-  for (int t = t0; t < t1; ++t) {
-    while (t >= end && s + 1 < p.seq.nseq) seq_span(p.seq, ++s, begin, end);
-    if (t == begin) {
-      const int slot = slot_of(p.slots, s);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (p.shift_in && slot >= 0)
-          load8<T>(p.shift_in, (size_t)slot * width + col[j], prev[j]);
-        else
-#pragma unroll
-          for (int i = 0; i < 8; ++i) prev[j][i] = 0.f;
+  // Each turn has row t in h, its mean, and row t + 1 on its way; one barrier
+  // sums row t's squares and row t + 1.
+  float h[NV][8], next[NV][8], prev[NV][8];
+  const int first = t0 > begin ? t0 - 1 : t0;
+  fetch(first);
+  sum(h);
+  if (first + 1 < t1) fetch(first + 1);
+  float v1[1] = {part_sum<NV>(h, on)};
+  block_sum(v1, red, buf, waves);
+  float mean = v1[0] * inv;
+  bool opened = false;  // the sequence at hand begins in this run
+  for (int t = first; t < t1; ++t) {
+    const bool more = t + 1 < t1;
+    if (more) {
+      sum(next);
+      if (t + 2 < t1) fetch(t + 2);
+    }
+    float v[2] = {part_squares<NV>(h, on, mean), more ? part_sum<NV>(next, on) : 0.f};
+    block_sum(v, red, buf, waves);
+    const float rstd = rsqrtf(v[0] * inv + p.eps);
+    if (t >= t0) {
+      while (t >= end && s + 1 < p.seq.nseq) {
+        seq_span(p.seq, ++s, begin, end);
+        opened = false;
       }
-      // the sequence's last row, by the workgroup that has read its shift_in,
-      // so that shift_out may be the same array
-      if (p.shift_out && slot >= 0 && end > begin) {
-        fetch(end - 1, h);
-        norm(h);
+      if (p.x_out)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (on[j]) store8<T>(p.x_out, (size_t)t * p.ld + col[j], h[j]);
+    }
+    norm(h, mean, rstd);
+    if (t >= t0) {
+      const int slot = slot_of(p.slots, s);
+      if (t == begin) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (p.shift_in && slot >= 0)
+            load8<T>(p.shift_in, (size_t)slot * width + col[j], prev[j]);
+          else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) prev[j][i] = 0.f;
+        }
+        opened = true;
+        // The sequence's last row, by the workgroup that has read its
+        // shift_in, so that shift_out may be the same array; here if it lies
+        // past this run, below if within.
+        if (p.shift_out && slot >= 0 && end > t1) {
+          float x[NV][8];
+          uint4 kx[NV], kd[NV];
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            kx[j] = rx[j];
+            kd[j] = rd[j];
+          }
+          fetch(end - 1);
+          sum(x);
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            rx[j] = kx[j];
+            rd[j] = kd[j];
+          }
+          float a[1] = {part_sum<NV>(x, on)};
+          block_sum(a, red, buf, waves);
+          const float m = a[0] * inv;
+          a[0] = part_squares<NV>(x, on, m);
+          block_sum(a, red, buf, waves);
+          norm(x, m, rsqrtf(a[0] * inv + p.eps));
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            if (on[j]) store8<T>(p.shift_out, (size_t)slot * width + col[j], x[j]);
+        }
+      }
+      if (t + 1 == end && opened && p.shift_out && slot >= 0)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (on[j]) store8<T>(p.shift_out, (size_t)slot * width + col[j], h[j]);
+      for (int i = 0; i < p.nmix; ++i) {
+        const float* mu = p.mu + (size_t)i * width;
+        void* out = (uint16_t*)p.out + ((size_t)i * p.seq.tokens + t) * p.ldo;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (!on[j]) continue;
+          float m[8];
+          load8f(mu + col[j], m);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) m[q] = fmaf(prev[j][q] - h[j][q], m[q], h[j][q]);
+          store8<T>(out, col[j], m);
+        }
       }
     }
-    fetch(t, h);
-    if (p.x_out)
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (on[j]) store8<T>(p.x_out, (size_t)t * p.ld + col[j], h[j]);
-    norm(h);
-    for (int i = 0; i < p.nmix; ++i) {
-      const float* mu = p.mu + (size_t)i * width;
-      void* out = (uint16_t*)p.out + ((size_t)i * p.seq.tokens + t) * p.ldo;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!on[j]) continue;
-        float m[8];
-        load8f(mu + col[j], m);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m[q] = fmaf(prev[j][q] - h[j][q], m[q], h[j][q]);
-        store8<T>(out, col[j], m);
-      }
-    }
+    mean = v[1] * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) prev[j][i] = h[j][i];
+      for (int i = 0; i < 8; ++i) {
+        prev[j][i] = h[j][i];
+        h[j][i] = next[j][i];
+      }
   }
 }
 
@@ -205,138 +285,188 @@ hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
 //   dgamma = sum dh n, dbeta = sum dh, dn = dh gamma,
 //   dx = dx_out + (dn - mean(dn) - n mean(dn n)) rstd,   ddelta = alpha dx
 // A workgroup walks its run of rows once and finishes row t - 1 when it has
-// p_t; it also reads the row after its run.  The parameter gradients stay in
+// p_t; it also reads the row after its run.  One barrier per row sums the four
+// values that three rows in different stages need.  Four channels per thread:
+// the sums of eight parameters' gradients and three rows take most of the 128
+// registers that a workgroup of 1024 has.  The parameter gradients stay in
 // registers over the run and are written as one row of partial sums, which a
 // second kernel adds in order.
 template <typename T, int NV, int NM>
-__global__ void __launch_bounds__(512) shift_norm_back_kernel(ShiftNormBack p, int rows) {
-  __shared__ float2 red[2][16];
+__global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, int rows) {
+  __shared__ __align__(16) float red[2][16][4];
   int buf = 0;
   const int waves = blockDim.x >> 6;
   const int width = p.width;
   int col[NV];
   bool on[NV];
-  float gamma[NV][8], beta[NV][8];
-  float dgamma[NV][8] = {}, dbeta[NV][8] = {}, dmu[NM][NV][8] = {};
+  float gamma[NV][4];
+  float dgamma[NV][4] = {}, dbeta[NV][4] = {}, dmu[NM][NV][4] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    col[j] = (j * blockDim.x + threadIdx.x) * 8;
+    col[j] = (j * blockDim.x + threadIdx.x) * 4;
     on[j] = col[j] < width;
     if (!on[j]) col[j] = 0;
-    load8f(p.gamma + col[j], gamma[j]);
-    load8f(p.beta + col[j], beta[j]);
+    load4f(p.gamma + col[j], gamma[j]);
   }
-  // n of row t and its 1 / sqrt(var + eps)
-  auto norm = [&](int t, float (*n)[8], float& rstd) {
-    float mean;
+  const float inv = 1.f / (float)width;
+  auto row = [&](int t, float (*x)[4]) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load8<T>(p.x, (size_t)t * p.ld + col[j], n[j]);
-    row_stats<NV>(n, on, width, p.eps, red, buf, waves, mean, rstd);
+    for (int j = 0; j < NV; ++j) load4<T>(p.x, (size_t)t * p.ld + col[j], x[j]);
+  };
+  auto norm = [&](float (*x)[4], float mean, float rstd) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[j][i] = (n[j][i] - mean) * rstd;
+      for (int i = 0; i < 4; ++i) x[j][i] = (x[j][i] - mean) * rstd;
   };
-
   const int t0 = blockIdx.x * rows, t1 = min(p.seq.tokens, t0 + rows);
-  // n and q of the row to finish, and its rstd
-  float n[NV][8], q[NV][8], rstd = 0.f;
   if (t0 < t1) {
     int s = seq_of(p.seq, t0), begin, end;
     seq_span(p.seq, s, begin, end);
-    if (t0 > begin) norm(t0 - 1, n, rstd);
+    // n, q and 1 / sqrt of the row to finish (t - 1); n of row t; row t + 1 with
+    // its mean; the planes of row t, and what finishes row t - 1, on their way
+    float n[NV][4], q[NV][4], nt[NV][4], x1[NV][4];
+    float rstd = 0.f, rstdt, mean1;
+    uint2 rd[NM][NV], rup[NV], rx[NV];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+        if (m < p.nmix)
+#pragma unroll
+          for (int j = 0; j < NV; ++j) rd[m][j] = raw4(p.dout, ((size_t)m * p.seq.tokens + t) * p.ldo + col[j]);
+    };
+    fetch(t0);
+    {
+      const bool before = t0 > begin;
+      row(before ? t0 - 1 : t0, n);
+      row(t0, nt);
+      if (t0 + 1 < t1) row(t0 + 1, x1);
+      float a[3] = {part_sum<NV>(n, on), part_sum<NV>(nt, on), t0 + 1 < t1 ? part_sum<NV>(x1, on) : 0.f};
+      block_sum(a, red, buf, waves);
+      float c[2] = {part_squares<NV>(n, on, a[0] * inv), part_squares<NV>(nt, on, a[1] * inv)};
+      block_sum(c, red, buf, waves);
+      rstd = rsqrtf(c[0] * inv + p.eps);
+      rstdt = rsqrtf(c[1] * inv + p.eps);
+      norm(n, a[0] * inv, rstd);
+      norm(nt, a[1] * inv, rstdt);
+      mean1 = a[2] * inv;
+    }
+    if (t0 + 2 < t1)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) rx[j] = raw4(p.x, (size_t)(t0 + 2) * p.ld + col[j]);
     for (int t = t0; t <= t1; ++t) {
       // gradients that reach row t and the row before it
-      float qt[NV][8] = {}, pt[NV][8] = {};
+      float qt[NV][4] = {}, pt[NV][4] = {};
       bool first = t == p.seq.tokens;
       if (!first) {
         while (t >= end && s + 1 < p.seq.nseq) seq_span(p.seq, ++s, begin, end);
         first = t == begin;
       }
-      float nt[NV][8], rstdt = 0.f;
-      if (t < t1) norm(t, nt, rstdt);
-      if (t < t1 || !first) {
+      const bool inside = t < t1;
+      if (inside || !first) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          float h[8] = {};
-          if (t < t1) {
+          float d0[4] = {};
+          if (inside) {
             // prev - h
             if (first) {
-              if (p.shift_in) load8<T>(p.shift_in, (size_t)s * width + col[j], h);
+              float beta[4];
+              load4f(p.beta + col[j], beta);
+              if (p.shift_in) load4<T>(p.shift_in, (size_t)s * width + col[j], d0);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) h[i] -= fmaf(nt[j][i], gamma[j][i], beta[j][i]);
+              for (int i = 0; i < 4; ++i) d0[i] -= fmaf(nt[j][i], gamma[j][i], beta[i]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) h[i] = (n[j][i] - nt[j][i]) * gamma[j][i];
+              for (int i = 0; i < 4; ++i) d0[i] = (n[j][i] - nt[j][i]) * gamma[j][i];
             }
           }
 #pragma unroll
           for (int m = 0; m < NM; ++m) {
             if (m < p.nmix) {
-              float d[8], mu[8];
-              load8<T>(p.dout, ((size_t)m * p.seq.tokens + t) * p.ldo + col[j], d);
-              load8f(p.mu + (size_t)m * width + col[j], mu);
+              float d[4], mu[4];
+              up4<T>(rd[m][j], d);
+              load4f(p.mu + (size_t)m * width + col[j], mu);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 pt[j][i] = fmaf(d[i], mu[i], pt[j][i]);
                 qt[j][i] += d[i];
-                if (t < t1) dmu[m][j][i] = fmaf(d[i], h[i], dmu[m][j][i]);
+                dmu[m][j][i] = fmaf(d[i], d0[i], dmu[m][j][i]);
               }
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) qt[j][i] -= pt[j][i];
-          if (t < t1 && first && p.dshift_in && on[j]) store8<T>(p.dshift_in, (size_t)s * width + col[j], pt[j]);
-          if (t < t1 && t + 1 == end && p.dshift_out) {
-            float d[8];
-            load8<T>(p.dshift_out, (size_t)s * width + col[j], d);
+          for (int i = 0; i < 4; ++i) qt[j][i] -= pt[j][i];
+          if (inside && first && p.dshift_in && on[j]) store4<T>(p.dshift_in, (size_t)s * width + col[j], pt[j]);
+          if (inside && t + 1 == end && p.dshift_out) {
+            float d[4];
+            load4<T>(p.dshift_out, (size_t)s * width + col[j], d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) qt[j][i] += d[i];
+            for (int i = 0; i < 4; ++i) qt[j][i] += d[i];
           }
         }
       }
+      // the next turn's planes (row t1's too, unless no token is there)
+      if (t + 1 <= t1 && t + 1 < p.seq.tokens) fetch(t + 1);
+      float v[4] = {};
       if (t > t0) {
-        // finish row t - 1
-        float m1 = 0.f, m2 = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (on[j])
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const float dh = first ? q[j][i] : q[j][i] + pt[j][i];
               dgamma[j][i] = fmaf(dh, n[j][i], dgamma[j][i]);
               dbeta[j][i] += dh;
               q[j][i] = dh * gamma[j][i];
-              m1 += q[j][i];
-              m2 = fmaf(q[j][i], n[j][i], m2);
+              v[0] += q[j][i];
+              v[1] = fmaf(q[j][i], n[j][i], v[1]);
             }
-        block_sum2(m1, m2, red, buf, waves);
-        m1 /= (float)width;
-        m2 /= (float)width;
+      }
+      float x2[NV][4];
+      if (t + 1 < t1) v[2] = part_squares<NV>(x1, on, mean1);
+      if (t + 2 < t1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) up4<T>(rx[j], x2[j]);
+        v[3] = part_sum<NV>(x2, on);
+        if (t + 3 < t1)
+#pragma unroll
+          for (int j = 0; j < NV; ++j) rx[j] = raw4(p.x, (size_t)(t + 3) * p.ld + col[j]);
+      }
+      block_sum(v, red, buf, waves);
+      if (t > t0) {
+        // finish row t - 1
+        const float m1 = v[0] * inv, m2 = v[1] * inv;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           if (!on[j]) continue;
           const size_t at = (size_t)(t - 1) * p.ld + col[j];
-          float d[8] = {};
-          if (p.dx_out) load8<T>(p.dx_out, at, d);
+          float d[4] = {};
+          if (p.dx_out) up4<T>(rup[j], d);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = fmaf(q[j][i] - m1 - n[j][i] * m2, rstd, d[i]);
-          store8<T>(p.dx, at, d);
+          for (int i = 0; i < 4; ++i) d[i] = fmaf(q[j][i] - m1 - n[j][i] * m2, rstd, d[i]);
+          store4<T>(p.dx, at, d);
           if (p.ddelta) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] *= p.alpha;
-            store8<T>(p.ddelta, at, d);
+            for (int i = 0; i < 4; ++i) d[i] *= p.alpha;
+            store4<T>(p.ddelta, at, d);
           }
         }
       }
+      if (inside && p.dx_out)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) rup[j] = raw4(p.dx_out, (size_t)t * p.ld + col[j]);
       rstd = rstdt;
+      rstdt = rsqrtf(v[2] * inv + p.eps);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           n[j][i] = nt[j][i];
           q[j][i] = qt[j][i];
+          nt[j][i] = (x1[j][i] - mean1) * rstdt;
+          x1[j][i] = x2[j][i];
         }
+      mean1 = v[3] * inv;
     }
   }
   // the empty sequences' shift gradients pass through; workgroup 0 does them
@@ -349,8 +479,8 @@ __global__ void __launch_bounds__(512) shift_norm_back_kernel(ShiftNormBack p, i
       for (int j = 0; j < NV; ++j) {
         if (!on[j]) continue;
         const size_t at = (size_t)i * width + col[j];
-        *(uint4*)((uint16_t*)p.dshift_in + at) =
-            p.dshift_out ? *(const uint4*)((const uint16_t*)p.dshift_out + at) : make_uint4(0, 0, 0, 0);
+        *(uint2*)((uint16_t*)p.dshift_in + at) =
+            p.dshift_out ? *(const uint2*)((const uint16_t*)p.dshift_out + at) : make_uint2(0, 0);
       }
     }
   const bool alone = gridDim.x == 1;
@@ -361,7 +491,6 @@ __global__ void __launch_bounds__(512) shift_norm_back_kernel(ShiftNormBack p, i
     auto put = [&](float* alone_to, int which, const float* f) {
       float* to = (alone ? alone_to : part + (size_t)which * width) + col[j];
       *(float4*)to = *(const float4*)f;
-      *(float4*)(to + 4) = *(const float4*)(f + 4);
     };
     put(p.dgamma, 0, dgamma[j]);
     put(p.dbeta, 1, dbeta[j]);
@@ -393,7 +522,7 @@ hipError_t launch_shift_norm_back(const ShiftNormBack& p, bool bf16, hipStream_t
   if (groups < 1) groups = 1;
   const int rows = (int)((p.seq.tokens + groups - 1) / groups);
   if (rows > 0) groups = (p.seq.tokens + rows - 1) / rows;
-  const dim3 grid((unsigned)groups), block(threads_of(p.width, nv));
+  const dim3 grid((unsigned)groups), block((p.width / 4 + nv * 64 - 1) / (nv * 64) * 64);
   if (bf16 && nv == 1)
     start_back<BF16, 1>(p, rows, grid, block, st);
   else if (bf16)
@@ -404,11 +533,7 @@ hipError_t launch_shift_norm_back(const ShiftNormBack& p, bool bf16, hipStream_t
     start_back<F16, 2>(p, rows, grid, block, st);
   hipError_t e = hipGetLastError();
   if (groups == 1 || e != hipSuccess) return e;
-  const size_t stride = (size_t)(2 + p.nmix) * p.width;
-  e = launch_sum_parts(p.parts, (int)groups, p.width, stride, p.dgamma, st);
-  if (e == hipSuccess) e = launch_sum_parts(p.parts + p.width, (int)groups, p.width, stride, p.dbeta, st);
-  if (e == hipSuccess) e = launch_sum_parts(p.parts + 2 * (size_t)p.width, (int)groups, p.nmix * p.width, stride, p.dmu, st);
-  return e;
+  return launch_sum_parts(p.parts, (int)groups, {{p.dgamma, p.dbeta, p.dmu}, {p.width, p.width, p.nmix * p.width}}, st);
 }
 
 }  // namespace rq

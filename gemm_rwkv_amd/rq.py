@@ -134,12 +134,22 @@ def _check(st, where):
         raise RqError(st, where)
 
 
+_gpu_seen = None
+
+
+def _gpu():
+    """Whether there is a GPU, asked once (the question takes microseconds)."""
+    global _gpu_seen
+    if _gpu_seen is None:
+        _gpu_seen = torch.cuda.is_available()
+    return _gpu_seen
+
+
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:  # an address, or None
         return t
-    return t.data_ptr()
 
 
 _default_ws = {}
@@ -172,18 +182,26 @@ def _ws(ws):
     if ws is False:
         return None, 0
     if ws is None:
-        if not torch.cuda.is_available():
+        if not _gpu():
             return None, 0
-        ws = default_workspace()
+        # one that exists needs no more than its device's number
+        ws = _default_ws.get(torch.cuda.current_device())
+        if ws is None:
+            ws = default_workspace()
     if isinstance(ws, tuple):
         return ws
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+# the current stream's handle by device number, without a Stream object where
+# this torch can say it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
         # without a GPU (argument checks only) there is no current stream
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        return _raw_stream(torch.cuda.current_device()) if _gpu() else None
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -385,7 +403,7 @@ def rq_gemm_int8_acc(xq, m, w, acc, stream=None, ws=None):
 def _fresh_ws(ws, nbytes, stream):
     """(pointer, bytes, tensor) of a workspace that must hold nbytes: the
     caller's, or, for None, memory of torch's allocator for this call."""
-    if ws is not None or not torch.cuda.is_available():
+    if ws is not None or not _gpu():
         return _ws(False if ws is None else ws) + (None,)
     t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     if stream is not None:
@@ -446,7 +464,8 @@ def rq_head_gate(dtype, y, r, k, v, g, tokens, heads, ld, gamma, beta, eps, u, o
     """(norm of each head of y * gamma + beta + (sum r k u) v) * g."""
     st = lib().rq_head_gate(dtype, _ptr(y), _ptr(r), _ptr(k), _ptr(v), _ptr(g), tokens, heads, ld, _ptr(gamma), _ptr(beta),
                             eps, _ptr(u), _ptr(out), ldo, _stream(stream))
-    _check(st, "rq_head_gate")
+    if st:
+        raise RqError(st, "rq_head_gate")
     return out
 
 
