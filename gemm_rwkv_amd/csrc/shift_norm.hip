@@ -72,14 +72,18 @@ __device__ __forceinline__ void up4(uint2 v, float* f) {
   up2<T>(v.x, f);
   up2<T>(v.y, f + 2);
 }
-__device__ __forceinline__ uint2 raw4(const void* base, size_t elem) { return *(const uint2*)((const uint16_t*)base + elem); }
-template <typename T>
-__device__ __forceinline__ void load4(const void* base, size_t elem, float* f) {
-  up4<T>(raw4(base, elem), f);
+// four channels of a row: the row's address is the same for all threads, so
+// that it lies in scalar registers
+__device__ __forceinline__ uint2 raw4(const void* base, size_t row, int col) {
+  return *(const uint2*)((const uint16_t*)base + row + (unsigned)col);
 }
 template <typename T>
-__device__ __forceinline__ void store4(void* base, size_t elem, const float* f) {
-  *(uint2*)((uint16_t*)base + elem) = make_uint2(T::down2(f[0], f[1]), T::down2(f[2], f[3]));
+__device__ __forceinline__ void load4(const void* base, size_t row, int col, float* f) {
+  up4<T>(raw4(base, row, col), f);
+}
+template <typename T>
+__device__ __forceinline__ void store4(void* base, size_t row, int col, const float* f) {
+  *(uint2*)((uint16_t*)base + row + (unsigned)col) = make_uint2(T::down2(f[0], f[1]), T::down2(f[2], f[3]));
 }
 __device__ __forceinline__ void load4f(const float* p, float* f) { *(float4*)f = *(const float4*)p; }
 __device__ __forceinline__ uint4 raw8(const void* base, size_t elem) { return *(const uint4*)((const uint16_t*)base + elem); }
@@ -292,7 +296,8 @@ hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
 // registers over the run and are written as one row of partial sums, which a
 // second kernel adds in order.
 template <typename T, int NV, int NM>
-__global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, int rows) {
+__global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, int rows, bool mu_lds) {
+  extern __shared__ __align__(16) float mus[];  // mu, if it fits: each row needs all of it
   __shared__ __align__(16) float red[2][16][4];
   int buf = 0;
   const int waves = blockDim.x >> 6;
@@ -308,10 +313,14 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
     if (!on[j]) col[j] = 0;
     load4f(p.gamma + col[j], gamma[j]);
   }
+  if (mu_lds) {
+    for (int i = threadIdx.x * 4; i < p.nmix * width; i += blockDim.x * 4) *(float4*)(mus + i) = *(const float4*)(p.mu + i);
+    __syncthreads();
+  }
   const float inv = 1.f / (float)width;
   auto row = [&](int t, float (*x)[4]) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load4<T>(p.x, (size_t)t * p.ld + col[j], x[j]);
+    for (int j = 0; j < NV; ++j) load4<T>(p.x, (size_t)t * p.ld, col[j], x[j]);
   };
   auto norm = [&](float (*x)[4], float mean, float rstd) {
 #pragma unroll
@@ -325,23 +334,31 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
     seq_span(p.seq, s, begin, end);
     // n, q and 1 / sqrt of the row to finish (t - 1); n of row t; row t + 1 with
     // its mean; the planes of row t, and what finishes row t - 1, on their way
-    float n[NV][4], q[NV][4], nt[NV][4], x1[NV][4];
+    float n[NV][4], q[NV][4], nt[NV][4];
+    uint2 r1[NV] = {};
     float rstd = 0.f, rstdt, mean1;
-    uint2 rd[NM][NV], rup[NV], rx[NV];
+    uint2 rd[NM][NV], rup[NV] = {}, rx[NV] = {};
     auto fetch = [&](int t) {
 #pragma unroll
       for (int m = 0; m < NM; ++m)
         if (m < p.nmix)
 #pragma unroll
-          for (int j = 0; j < NV; ++j) rd[m][j] = raw4(p.dout, ((size_t)m * p.seq.tokens + t) * p.ldo + col[j]);
+          for (int j = 0; j < NV; ++j) rd[m][j] = raw4(p.dout, ((size_t)m * p.seq.tokens + t) * p.ldo, col[j]);
     };
     fetch(t0);
     {
       const bool before = t0 > begin;
       row(before ? t0 - 1 : t0, n);
       row(t0, nt);
-      if (t0 + 1 < t1) row(t0 + 1, x1);
-      float a[3] = {part_sum<NV>(n, on), part_sum<NV>(nt, on), t0 + 1 < t1 ? part_sum<NV>(x1, on) : 0.f};
+      float x1[NV][4] = {};
+      if (t0 + 1 < t1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          r1[j] = raw4(p.x, (size_t)(t0 + 1) * p.ld, col[j]);
+          up4<T>(r1[j], x1[j]);
+        }
+      }
+      float a[3] = {part_sum<NV>(n, on), part_sum<NV>(nt, on), part_sum<NV>(x1, on)};
       block_sum(a, red, buf, waves);
       float c[2] = {part_squares<NV>(n, on, a[0] * inv), part_squares<NV>(nt, on, a[1] * inv)};
       block_sum(c, red, buf, waves);
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
     }
     if (t0 + 2 < t1)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) rx[j] = raw4(p.x, (size_t)(t0 + 2) * p.ld + col[j]);
+      for (int j = 0; j < NV; ++j) rx[j] = raw4(p.x, (size_t)(t0 + 2) * p.ld, col[j]);
     for (int t = t0; t <= t1; ++t) {
       // gradients that reach row t and the row before it
       float qt[NV][4] = {}, pt[NV][4] = {};
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
             if (first) {
               float beta[4];
               load4f(p.beta + col[j], beta);
-              if (p.shift_in) load4<T>(p.shift_in, (size_t)s * width + col[j], d0);
+              if (p.shift_in) load4<T>(p.shift_in, (size_t)s * width, col[j], d0);
 #pragma unroll
               for (int i = 0; i < 4; ++i) d0[i] -= fmaf(nt[j][i], gamma[j][i], beta[i]);
             } else {
@@ -385,7 +402,7 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
             if (m < p.nmix) {
               float d[4], mu[4];
               up4<T>(rd[m][j], d);
-              load4f(p.mu + (size_t)m * width + col[j], mu);
+              load4f((mu_lds ? mus : p.mu) + (size_t)m * width + (unsigned)col[j], mu);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 pt[j][i] = fmaf(d[i], mu[i], pt[j][i]);
@@ -396,10 +413,10 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) qt[j][i] -= pt[j][i];
-          if (inside && first && p.dshift_in && on[j]) store4<T>(p.dshift_in, (size_t)s * width + col[j], pt[j]);
+          if (inside && first && p.dshift_in && on[j]) store4<T>(p.dshift_in, (size_t)s * width, col[j], pt[j]);
           if (inside && t + 1 == end && p.dshift_out) {
             float d[4];
-            load4<T>(p.dshift_out, (size_t)s * width + col[j], d);
+            load4<T>(p.dshift_out, (size_t)s * width, col[j], d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) qt[j][i] += d[i];
           }
@@ -422,15 +439,16 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
               v[1] = fmaf(q[j][i], n[j][i], v[1]);
             }
       }
-      float x2[NV][4];
-      if (t + 1 < t1) v[2] = part_squares<NV>(x1, on, mean1);
+      float x[NV][4];
+      if (t + 1 < t1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) up4<T>(r1[j], x[j]);
+        v[2] = part_squares<NV>(x, on, mean1);
+      }
       if (t + 2 < t1) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) up4<T>(rx[j], x2[j]);
-        v[3] = part_sum<NV>(x2, on);
-        if (t + 3 < t1)
-#pragma unroll
-          for (int j = 0; j < NV; ++j) rx[j] = raw4(p.x, (size_t)(t + 3) * p.ld + col[j]);
+        for (int j = 0; j < NV; ++j) up4<T>(rx[j], x[j]);
+        v[3] = part_sum<NV>(x, on);
       }
       block_sum(v, red, buf, waves);
       if (t > t0) {
@@ -439,33 +457,36 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           if (!on[j]) continue;
-          const size_t at = (size_t)(t - 1) * p.ld + col[j];
+          const size_t at = (size_t)(t - 1) * p.ld;
           float d[4] = {};
           if (p.dx_out) up4<T>(rup[j], d);
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[i] = fmaf(q[j][i] - m1 - n[j][i] * m2, rstd, d[i]);
-          store4<T>(p.dx, at, d);
+          store4<T>(p.dx, at, col[j], d);
           if (p.ddelta) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] *= p.alpha;
-            store4<T>(p.ddelta, at, d);
+            store4<T>(p.ddelta, at, col[j], d);
           }
         }
       }
       if (inside && p.dx_out)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) rup[j] = raw4(p.dx_out, (size_t)t * p.ld + col[j]);
+        for (int j = 0; j < NV; ++j) rup[j] = raw4(p.dx_out, (size_t)t * p.ld, col[j]);
       rstd = rstdt;
       rstdt = rsqrtf(v[2] * inv + p.eps);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        up4<T>(r1[j], x[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           n[j][i] = nt[j][i];
           q[j][i] = qt[j][i];
-          nt[j][i] = (x1[j][i] - mean1) * rstdt;
-          x1[j][i] = x2[j][i];
+          nt[j][i] = (x[j][i] - mean1) * rstdt;
         }
+        r1[j] = rx[j];
+        if (t + 3 < t1) rx[j] = raw4(p.x, (size_t)(t + 3) * p.ld, col[j]);
+      }
       mean1 = v[3] * inv;
     }
   }
@@ -501,14 +522,23 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
 }
 
 namespace {
+template <typename T, int NV, int NM>
+hipError_t start_back(const ShiftNormBack& p, int rows, dim3 grid, dim3 block, hipStream_t st) {
+  // mu in LDS up to six planes of 4096 channels; a larger one stays in L2
+  constexpr int kMost = 96 * 1024;
+  const size_t bytes = (size_t)p.nmix * p.width * 4;
+  const bool mu_lds = bytes <= kMost;
+  static const hipError_t attr =
+      hipFuncSetAttribute((const void*)shift_norm_back_kernel<T, NV, NM>, hipFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((shift_norm_back_kernel<T, NV, NM>), grid, block, mu_lds ? bytes : 0, st, p, rows, mu_lds);
+  return hipGetLastError();
+}
 template <typename T, int NV>
-void start_back(const ShiftNormBack& p, int rows, dim3 grid, dim3 block, hipStream_t st) {
-  if (p.nmix == 1)
-    hipLaunchKernelGGL((shift_norm_back_kernel<T, NV, 1>), grid, block, 0, st, p, rows);
-  else if (p.nmix <= 6)
-    hipLaunchKernelGGL((shift_norm_back_kernel<T, NV, 6>), grid, block, 0, st, p, rows);
-  else
-    hipLaunchKernelGGL((shift_norm_back_kernel<T, NV, 8>), grid, block, 0, st, p, rows);
+hipError_t start_back(const ShiftNormBack& p, int rows, dim3 grid, dim3 block, hipStream_t st) {
+  if (p.nmix == 1) return start_back<T, NV, 1>(p, rows, grid, block, st);
+  if (p.nmix <= 6) return start_back<T, NV, 6>(p, rows, grid, block, st);
+  return start_back<T, NV, 8>(p, rows, grid, block, st);
 }
 }  // namespace
 
@@ -523,15 +553,8 @@ hipError_t launch_shift_norm_back(const ShiftNormBack& p, bool bf16, hipStream_t
   const int rows = (int)((p.seq.tokens + groups - 1) / groups);
   if (rows > 0) groups = (p.seq.tokens + rows - 1) / rows;
   const dim3 grid((unsigned)groups), block((p.width / 4 + nv * 64 - 1) / (nv * 64) * 64);
-  if (bf16 && nv == 1)
-    start_back<BF16, 1>(p, rows, grid, block, st);
-  else if (bf16)
-    start_back<BF16, 2>(p, rows, grid, block, st);
-  else if (nv == 1)
-    start_back<F16, 1>(p, rows, grid, block, st);
-  else
-    start_back<F16, 2>(p, rows, grid, block, st);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = bf16 ? (nv == 1 ? start_back<BF16, 1>(p, rows, grid, block, st) : start_back<BF16, 2>(p, rows, grid, block, st))
+                            : (nv == 1 ? start_back<F16, 1>(p, rows, grid, block, st) : start_back<F16, 2>(p, rows, grid, block, st));
   if (groups == 1 || e != hipSuccess) return e;
   return launch_sum_parts(p.parts, (int)groups, {{p.dgamma, p.dbeta, p.dmu}, {p.width, p.width, p.nmix * p.width}}, st);
 }
