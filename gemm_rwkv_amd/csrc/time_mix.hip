@@ -9,6 +9,8 @@
 // sixteen of them; a row lies across sixteen lanes, four columns each, and the
 // sums S a and S r are four lane rotations.  A run of up to sixteen tokens is
 // staged in LDS as fp32.
+#include <climits>
+
 #include "mix.h"
 #include "time_mix_chunk.h"
 
@@ -19,7 +21,7 @@ constexpr int kRun = 16;  // tokens staged at once
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p) {
+__global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p, int most) {
   // r, w (as decay), k, v, a, b of the run, then y
   __shared__ __align__(16) float in[6][kRun][kHead];
   __shared__ float out[kRun][kHead];
@@ -27,6 +29,7 @@ __global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int begin, end;
   seq_span(p.seq, s, begin, end);
+  if (end - begin > most) return;
   const int slot = slot_of(p.slots, s);
   const size_t state = ((size_t)(slot < 0 ? 0 : slot) * p.heads + head) * kHead * kHead;
   // rows row + 4 j, columns col .. col + 3
@@ -143,14 +146,14 @@ __device__ __forceinline__ bool find_segment(const Sequences& s, int len, int id
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chunk_kernel(TimeMix p, SegmentSplit split) {
+__global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chunk_kernel(TimeMix p, SegmentSplit split, int over) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Segment sg;
-  if (!find_segment(p.seq, split.len, idx, sg)) return;
+  if (!find_segment(p.seq, split.len, idx, sg) || sg.end - sg.begin <= over) return;
   clear_counts(sh);
   if (wave >= 4) {
     prepare_chunks<T, false, kPreps>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
@@ -227,7 +230,10 @@ __global__ void __launch_bounds__(walk_threads(kMapPreps)) time_mix_segment_kern
 namespace {
 // Tokens per segment, or 0 for none.  A cut sequence costs about 2.4 times
 // the work, so it pays only from four segments on; they are made to fill the
-// 256 compute units once, and are at least 128 tokens long.
+// 256 compute units once, and are at least 128 tokens long.  Measured for one
+// sequence, whole against cut: 32 heads, 512 tokens 43 and 39 us, 4096 291 and
+// 113; 64 heads, 512 tokens 43 and 42, 4096 292 and 188; 128 heads, two
+// segments each, 512 tokens 45 and 57, 4096 297 and 332; 256 tokens 25 and 34.
 int segment_len(const TimeMix& p) {
   const int64_t chains = (int64_t)p.seq.nseq * p.heads;
   const int64_t mean = p.seq.tokens / p.seq.nseq;
@@ -241,28 +247,47 @@ int segment_len(const TimeMix& p) {
   return (int)len;
 }
 
+// Sequences of more than `over` tokens (-1: all).
 template <typename T>
-hipError_t start_chunks(const TimeMix& p, hipStream_t st) {
+hipError_t start_chunks(const TimeMix& p, int over, hipStream_t st) {
   static const hipError_t attr = allow_lds(time_mix_chunk_kernel<T>);
   static const hipError_t attr2 = allow_lds(time_mix_segment_kernel<T>);
   if (attr != hipSuccess || attr2 != hipSuccess) return attr != hipSuccess ? attr : attr2;
-  SegmentSplit split = {segment_len(p), p.parts};
+  SegmentSplit split = {over < 0 ? segment_len(p) : 0, p.parts};
   const unsigned chains = (unsigned)(split.len ? p.seq.tokens / split.len + p.seq.nseq : p.seq.nseq) * p.heads;
   if (split.len)
     hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(walk_threads(kMapPreps)), sizeof(ChunkLds), st, p, split);
-  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(walk_threads(kPreps)), sizeof(ChunkLds), st, p, split);
+  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(walk_threads(kPreps)), sizeof(ChunkLds), st, p, split, over);
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t start_time_mix(const TimeMix& p, hipStream_t st) {
+  // A chunk workgroup has a compute unit to itself and takes 7.5 us for up to
+  // 16 tokens, a step workgroup 3 + 0.4 us a token, and eight of those share a
+  // unit.  Measured at 32 heads, steps against chunks: 1 sequence of 8 tokens
+  // 6.1 and 7.6 us, of 12 7.6 and 7.7, of 16 9.1 and 7.7; 32 sequences of 4
+  // 9.3 and 28, of 24 30 and 35, of 32 38 and 36.
+  const int64_t chains = (int64_t)p.seq.nseq * p.heads;
+  const dim3 grid((unsigned)chains), block(256);
+  if (p.seq.tokens <= p.seq.nseq || p.seq.tokens <= 12) {
+    hipLaunchKernelGGL(time_mix_step_kernel<T>, grid, block, 0, st, p, INT_MAX);
+    return hipGetLastError();
+  }
+  // Where the chunk workgroups would queue, the short sequences of a batch of
+  // mostly short ones take steps and only the others chunks.
+  constexpr int kShort = 24;
+  if (chains > 256 && p.seq.tokens <= (int64_t)kShort * p.seq.nseq) {
+    hipLaunchKernelGGL(time_mix_step_kernel<T>, grid, block, 0, st, p, kShort);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || p.seq.tokens <= kShort ? e : start_chunks<T>(p, kShort, st);
+  }
+  return start_chunks<T>(p, -1, st);
 }
 }  // namespace
 
 hipError_t launch_time_mix(const TimeMix& p, bool bf16, hipStream_t st) {
-  const dim3 grid((unsigned)p.seq.nseq * p.heads), block(256);
-  if (p.seq.tokens > p.seq.nseq) return bf16 ? start_chunks<BF16>(p, st) : start_chunks<F16>(p, st);
-  if (bf16)
-    hipLaunchKernelGGL(time_mix_step_kernel<BF16>, grid, block, 0, st, p);
-  else
-    hipLaunchKernelGGL(time_mix_step_kernel<F16>, grid, block, 0, st, p);
-  return hipGetLastError();
+  return bf16 ? start_time_mix<BF16>(p, st) : start_time_mix<F16>(p, st);
 }
 
 }  // namespace rq

@@ -297,8 +297,43 @@ struct ChunkPrep {
     o.v[1][block] = t[1];
   }
 
-  __device__ __forceinline__ static float lane_of(float v, int lane) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  // Rows 0..15 of a 16x16 result, each in one register of every lane group:
+  // lane swaps of the halves, then of the quarters.
+  __device__ __forceinline__ static void spread_rows(float4v x, float* row) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = x[i];  // a vector's element is not cast in place: clang takes the first one
+      const uint32_t v = __builtin_bit_cast(uint32_t, f);
+      const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // groups 0 1 0 1, 2 3 2 3
+      const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+      row[i] = __builtin_bit_cast(float, (uint32_t)lo[0]);
+      row[4 + i] = __builtin_bit_cast(float, (uint32_t)lo[1]);
+      row[8 + i] = __builtin_bit_cast(float, (uint32_t)hi[0]);
+      row[12 + i] = __builtin_bit_cast(float, (uint32_t)hi[1]);
+    }
+  }
+  // x + lane LANE of each group's v * y
+  template <int LANE>
+  __device__ __forceinline__ static float fma_lane(float v, float y, float x) {
+    return fmaf(dpp<0x150 + LANE>(v), y, x);  // row_newbcast
+  }
+  template <int S, int U, bool COLUMN>
+  __device__ __forceinline__ static float substitute(const float* ab, const float* row, float x) {
+    // row form: T[q][s] += T[q][u] Ab[u][s], u from 15 down to s + 1; column
+    // form: T[s][q] += Ab[s][u] T[u][q], u from 0 up to s - 1
+    if constexpr (COLUMN) {
+      if constexpr (U < S) return substitute<S, U + 1, true>(ab, row, fma_lane<U>(ab[S], row[U], x));
+    } else {
+      if constexpr (U > S) return substitute<S, U - 1, false>(ab, row, fma_lane<S>(ab[U], row[U], x));
+    }
+    return x;
+  }
+  template <int S, bool COLUMN>
+  __device__ __forceinline__ static void substitute_all(const float* ab, float* row, int q) {
+    row[S] = substitute<S, COLUMN ? 0 : 15, COLUMN>(ab, row, q == S ? 1.f : 0.f);
+    if constexpr (COLUMN && S < 15) substitute_all<S + 1, true>(ab, row, q);
+    if constexpr (!COLUMN && S > 0) substitute_all<S - 1, false>(ab, row, q);
   }
   __device__ __forceinline__ static float4v pick4(const float* x, int g) {
     float4v r;
@@ -317,24 +352,9 @@ struct ChunkPrep {
   // Ab grow and cancel where neighbouring tokens share a direction.
   __device__ __forceinline__ void solve(ChunkOps& o, int lane) const {
     const int q = lane & 15, g = lane >> 4;
-    float row[16];
-    if (REV) {
-#pragma unroll
-      for (int s = 0; s < 16; ++s) {
-        float x = q == s ? 1.f : 0.f;
-#pragma unroll
-        for (int u = 0; u < s; ++u) x = fmaf(row[u], lane_of(ab[s & 3], 16 * (s >> 2) + u), x);
-        row[s] = x;
-      }
-    } else {
-#pragma unroll
-      for (int s = 15; s >= 0; --s) {
-        float x = q == s ? 1.f : 0.f;
-#pragma unroll
-        for (int u = 15; u > s; --u) x = fmaf(row[u], lane_of(ab[u & 3], 16 * (u >> 2) + s), x);
-        row[s] = x;
-      }
-    }
+    float row[16], abr[16];
+    spread_rows(ab, abr);
+    substitute_all<REV ? 0 : 15, REV>(abr, row, q);
     uint2 t[3];
     split4<3>(pick4(row, g), t);
 #pragma unroll

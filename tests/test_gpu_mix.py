@@ -101,7 +101,19 @@ LENS = [[1], [2], [15], [16], [17], [31, 33], [0, 5, 0, 1, 40, 0], [64, 1, 65], 
 @pytest.mark.parametrize("lens", LENS, ids=str)
 @pytest.mark.parametrize("ws", [None, False], ids=["ws", "none"])
 def test_time_mix(lens, code, ws):
-    heads = 1 if max(lens) > 500 else 3
+    check_time_mix(lens, 1 if max(lens) > 500 else 3, code, ws)
+
+
+# several sequences cut into segments; batches of mostly short sequences, of
+# which some, or none, are longer than the step kernel takes there
+@pytest.mark.parametrize("code", TYPES, ids=IDS)
+@pytest.mark.parametrize("lens,heads", [([700, 0, 900], 2), ([1, 24, 25, 0, 70, 2] * 8, 6), ([3] * 300, 1)],
+                         ids=["segments", "short and long", "short"])
+def test_time_mix_batches(lens, heads, code):
+    check_time_mix(lens, heads, code, None)
+
+
+def check_time_mix(lens, heads, code, ws):
     c, ld = 64 * heads, 64 * heads + 8
     t, n = sum(lens), len(lens)
     say("time_mix", lens, code, heads, ws)
