@@ -96,30 +96,29 @@ __global__ void __launch_bounds__(256) time_mix_step_kernel(TimeMix p, int most)
 // Where a workgroup is: a sequence, or a segment of one.
 //
 // A sequence is a chain of chunks, and few sequences and heads leave most of
-// the GPU idle.  Then each is cut into segments of `len` tokens.  The state
-// after a segment is S P + G, where G is what the segment leaves of a zero
-// state and P its map of the 64 channels of k; both are the recurrence itself,
-// started from zeros and from the identity (without v).  A first launch makes
-// G and P of every segment but the last ones, all at once (the first segment
-// starts from its real state and needs no P); in the second each segment
-// builds the state before it from those and then walks its chunks.
+// the GPU idle.  Then each is cut into segments.  The state after a segment is
+// S P + G, where G is what the segment leaves of a zero state and P its map of
+// the 64 channels of k; both are the recurrence itself, started from zeros and
+// from the identity (without v).  A first launch makes G and P of every middle
+// segment, all at once, and walks the first one, which has its real state, to
+// its end; in the second each later segment builds the state before it from
+// those and then walks its chunks.  The walk with the map takes half as long
+// again, so the first segment is longer, and both launches are level.
 struct SegmentSplit {
   int len;        // tokens per segment, a multiple of 16; 0: whole sequences
+  int first;      // tokens of a sequence's first segment, another one
   float* states;  // [segments][heads][G, P][64][64]
 };
 
 namespace {
-constexpr int kPreps = 8;     // preparing waves
-constexpr int kMapPreps = 4;  // with two states per wave, which take more registers
-
 struct Segment {
   int seq, begin, end;
   int nth, of;  // which of the sequence's segments
 };
 
 // Workgroup `idx`'s segment; false past the last one.
-__device__ __forceinline__ bool find_segment(const Sequences& s, int len, int idx, Segment& g) {
-  if (!len) {
+__device__ __forceinline__ bool find_segment(const Sequences& s, const SegmentSplit& split, int idx, Segment& g) {
+  if (!split.len) {
     g.seq = idx;
     g.nth = 0;
     g.of = 1;
@@ -129,13 +128,13 @@ __device__ __forceinline__ bool find_segment(const Sequences& s, int len, int id
   for (int i = 0; i < s.nseq; ++i) {
     int b, e;
     seq_span(s, i, b, e);
-    const int n = max(1, (e - b + len - 1) / len);
+    const int n = 1 + max(0, e - b - split.first + split.len - 1) / split.len;
     if (idx < n) {
       g.seq = i;
       g.nth = idx;
       g.of = n;
-      g.begin = b + idx * len;
-      g.end = min(e, g.begin + len);
+      g.begin = idx ? b + split.first + (idx - 1) * split.len : b;
+      g.end = min(e, b + split.first + idx * split.len);
       return true;
     }
     idx -= n;
@@ -143,40 +142,14 @@ __device__ __forceinline__ bool find_segment(const Sequences& s, int len, int id
   return false;
 }
 
-}  // namespace
-
+// Walks a segment's chunks from the state before it, writing y.
 template <typename T>
-__global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chunk_kernel(TimeMix p, SegmentSplit split, int over) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  ChunkLds& sh = *(ChunkLds*)lds;
-  const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Segment sg;
-  if (!find_segment(p.seq, split.len, idx, sg) || sg.end - sg.begin <= over) return;
-  clear_counts(sh);
-  if (wave >= 4) {
-    prepare_chunks<T, false, kPreps>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
-    return;
-  }
-  const int slot = slot_of(p.slots, sg.seq);
-  const size_t state = ((size_t)(slot < 0 ? 0 : slot) * p.heads + head) * kHead * kHead;
-  ChunkState st;
-  if (sg.of == 1) {
-    st.load(p.state_in && slot >= 0 ? p.state_in + state : nullptr, wave, lane);
-  } else {
-    // The segments of this sequence begin at workgroup idx - nth.  The first
-    // one's P holds the sequence's own state: state_out may be state_in, and
-    // the last segment may be done before the first one starts.
-    const size_t pair = 2 * kHead * kHead, stride = p.heads * pair;
-    const float* at = split.states + (size_t)(idx - sg.nth) * stride + head * pair;
-    st.load(sg.nth ? at : at + kHead * kHead, wave, lane);
-    for (int i = 1; i < sg.nth; ++i) st.apply(at + i * stride, at + i * stride + kHead * kHead, wave, lane);
-  }
+__device__ __forceinline__ void walk_out(const TimeMix& p, const Segment& sg, ChunkState& st, ChunkLds& sh, int head, int wave,
+                                         int lane) {
   const int chunks = (sg.end - sg.begin + kChunk - 1) / kChunk;
   const int q = lane & 15, g = lane >> 4;
   uint16_t* to = (uint16_t*)p.y + (size_t)(sg.begin + 4 * g) * p.ldy + head * kHead + 16 * wave + q;
-  walk_chunks<T, 1, true, false>(&st, chunks, sh, wave, lane, [](int) {}, [](int, float4v) {}, [&](int c, float4v y) {
+  walk_chunks<T, true, false>(st, chunks, sh, wave, lane, ~0u, [](int) {}, [](int, float4v) {}, [&](int c, float4v y) {
     const int left = sg.end - sg.begin - c * kChunk;
     const uint32_t y01 = T::down2(y[0], y[1]), y23 = T::down2(y[2], y[3]);
     if (left >= kChunk) {
@@ -191,60 +164,103 @@ __global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chunk_kernel(Ti
     }
     to += (size_t)kChunk * p.ldy;
   });
-  if (p.state_out && slot >= 0 && sg.nth + 1 == sg.of) st.store(p.state_out + state, wave, lane);
 }
 
-// G and P of a segment; of a first one the state after it, and before it.
+__device__ __forceinline__ size_t state_at(const TimeMix& p, int slot, int head) {
+  return ((size_t)(slot < 0 ? 0 : slot) * p.heads + head) * kHead * kHead;
+}
+}  // namespace
+
 template <typename T>
-__global__ void __launch_bounds__(walk_threads(kMapPreps)) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
+__global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chunk_kernel(TimeMix p, SegmentSplit split, int over) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Segment sg;
-  if (!find_segment(p.seq, split.len, idx, sg) || sg.nth + 1 == sg.of) return;
+  if (!find_segment(p.seq, split, idx, sg) || sg.end - sg.begin <= over || (sg.nth == 0 && sg.of > 1)) return;
   clear_counts(sh);
   if (wave >= 4) {
-    prepare_chunks<T, false, kMapPreps>(p, sg.begin, sg.end, sh, head, wave - 4, lane);
+    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, 4, wave, lane);
     return;
   }
   const int slot = slot_of(p.slots, sg.seq);
-  const int chunks = (sg.end - sg.begin) / kChunk;  // whole: only a last segment is ragged
-  auto none = [](int, float4v) {};
-  float* to = split.states + ((size_t)idx * p.heads + head) * 2 * kHead * kHead;
-  ChunkState st[2];
-  if (sg.nth == 0) {
-    st[0].load(p.state_in && slot >= 0 ? p.state_in + ((size_t)slot * p.heads + head) * kHead * kHead : nullptr, wave, lane);
-    st[0].store(to + kHead * kHead, wave, lane);
-    walk_chunks<T, 1, false, false>(st, chunks, sh, wave, lane, [](int) {}, none, none);
+  const size_t state = state_at(p, slot, head);
+  ChunkState st;
+  if (sg.of == 1) {
+    st.load(p.state_in && slot >= 0 ? p.state_in + state : nullptr, wave, lane);
   } else {
-    st[0].load(nullptr, wave, lane);
-    st[1].identity(wave, lane);
-    walk_chunks<T, 2, false, false>(st, chunks, sh, wave, lane, [](int) {}, none, none);
-    st[1].store(to + kHead * kHead, wave, lane);
+    // the segments of this sequence begin at workgroup idx - nth
+    const size_t pair = 2 * kHead * kHead, stride = p.heads * pair;
+    const float* at = split.states + (size_t)(idx - sg.nth) * stride + head * pair;
+    st.load(at, wave, lane);
+    for (int i = 1; i < sg.nth; ++i) st.apply(at + i * stride, at + i * stride + kHead * kHead, wave, lane);
   }
-  st[0].store(to, wave, lane);
+  walk_out<T>(p, sg, st, sh, head, wave, lane);
+  if (p.state_out && slot >= 0 && sg.nth + 1 == sg.of) st.store(p.state_out + state, wave, lane);
+}
+
+// The first segment with its outputs, G and P of the middle ones.
+template <typename T>
+__global__ void __launch_bounds__(64 * kWalkWaves) time_mix_segment_kernel(TimeMix p, SegmentSplit split) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  ChunkLds& sh = *(ChunkLds*)lds;
+  const int head = blockIdx.x % p.heads, idx = blockIdx.x / p.heads;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Segment sg;
+  if (!find_segment(p.seq, split, idx, sg) || sg.nth + 1 == sg.of) return;
+  clear_counts(sh);
+  const int walkers = sg.nth ? 8 : 4;  // the state, and the map
+  if (wave >= walkers) {
+    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, walkers, wave, lane);
+    return;
+  }
+  float* to = split.states + ((size_t)idx * p.heads + head) * 2 * kHead * kHead;
+  ChunkState st;
+  if (sg.nth == 0) {
+    const int slot = slot_of(p.slots, sg.seq);
+    st.load(p.state_in && slot >= 0 ? p.state_in + state_at(p, slot, head) : nullptr, wave, lane);
+    walk_out<T>(p, sg, st, sh, head, wave, lane);
+    st.store(to, wave, lane);
+    return;
+  }
+  const bool map = wave >= 4;
+  const int part = wave & 3;
+  if (map)
+    st.identity(part, lane);
+  else
+    st.load(nullptr, part, lane);
+  auto none = [](int, float4v) {};
+  const int chunks = (sg.end - sg.begin) / kChunk;  // whole: only a last segment is ragged
+  walk_chunks<T, false, false>(st, chunks, sh, part, lane, map ? 0u : ~0u, [](int) {}, none, none);
+  st.store(to + (map ? kHead * kHead : 0), part, lane);
 }
 
 namespace {
-// Tokens per segment, or 0 for none.  A cut sequence costs about 2.4 times
-// the work, so it pays only from four segments on; they are made to fill the
-// 256 compute units once, and are at least 128 tokens long.  Measured for one
-// sequence, whole against cut: 32 heads, 512 tokens 43 and 39 us, 4096 291 and
-// 113; 64 heads, 512 tokens 43 and 42, 4096 292 and 188; 128 heads, two
-// segments each, 512 tokens 45 and 57, 4096 297 and 332; 256 tokens 25 and 34.
-int segment_len(const TimeMix& p) {
+// How sequences are cut: len 0 for not at all.  A middle segment is walked
+// three times over, twice by itself and once by its map, so cutting pays only
+// from four segments on; they are made to fill the 256 compute units once in
+// each launch, and are at least 128 tokens long.  Measured for one sequence,
+// whole against cut: 32 heads, 512 tokens 43 and 43 us, 1024 78 and 52, 4096
+// 291 and 124; 64 heads, 512 tokens 43 and 45, 1024 79 and 64, 4096 292 and
+// 181; 128 heads in two segments each (without the map), 512 tokens 45 and 57,
+// 4096 297 and 332; 32 heads, 256 tokens 25 and 34.  First segments of 1 to 2
+// times the others' length are within 5% of each other.
+SegmentSplit segment_split(const TimeMix& p) {
+  const SegmentSplit whole = {0, 0, nullptr};
   const int64_t chains = (int64_t)p.seq.nseq * p.heads;
   const int64_t mean = p.seq.tokens / p.seq.nseq;
   const int64_t want = 256 / chains;
-  if (want < 4 || mean < 4 * 128) return 0;
-  int64_t len = (mean + want - 1) / want;
+  if (want < 4 || mean < 4 * 128) return whole;
+  // each launch leaves out one segment: first + want * len tokens
+  int64_t len = (2 * mean + 2 * want + 2) / (2 * want + 3);
   if (len < 128) len = 128;
   len = (len + kChunk - 1) / kChunk * kChunk;
   const int64_t segments = p.seq.tokens / len + p.seq.nseq;
-  if (!p.parts || (size_t)segments * p.heads * 2 * kHead * kHead * 4 > p.parts_bytes) return 0;
-  return (int)len;
+  if (!p.parts || (size_t)segments * p.heads * 2 * kHead * kHead * 4 > p.parts_bytes) return whole;
+  return {(int)len, (int)(len * 3 / 2 / kChunk * kChunk), p.parts};
 }
 
 // Sequences of more than `over` tokens (-1: all).
@@ -253,11 +269,11 @@ hipError_t start_chunks(const TimeMix& p, int over, hipStream_t st) {
   static const hipError_t attr = allow_lds(time_mix_chunk_kernel<T>);
   static const hipError_t attr2 = allow_lds(time_mix_segment_kernel<T>);
   if (attr != hipSuccess || attr2 != hipSuccess) return attr != hipSuccess ? attr : attr2;
-  SegmentSplit split = {over < 0 ? segment_len(p) : 0, p.parts};
+  const SegmentSplit split = over < 0 ? segment_split(p) : SegmentSplit{0, 0, nullptr};
   const unsigned chains = (unsigned)(split.len ? p.seq.tokens / split.len + p.seq.nseq : p.seq.nseq) * p.heads;
   if (split.len)
-    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(walk_threads(kMapPreps)), sizeof(ChunkLds), st, p, split);
-  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(walk_threads(kPreps)), sizeof(ChunkLds), st, p, split, over);
+    hipLaunchKernelGGL(time_mix_segment_kernel<T>, dim3(chains), dim3(64 * kWalkWaves), sizeof(ChunkLds), st, p, split);
+  hipLaunchKernelGGL(time_mix_chunk_kernel<T>, dim3(chains), dim3(64 * kWalkWaves), sizeof(ChunkLds), st, p, split, over);
   return hipGetLastError();
 }
 

@@ -25,7 +25,6 @@
 namespace rq {
 
 namespace {
-constexpr int kPreps = 8;  // preparing waves of a chain
 constexpr int kState = kHead * kHead;
 
 // Chunk c of sequence s is number begin / 16 + s + c of all chunks: at least
@@ -56,7 +55,7 @@ struct Chain {
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chains_kernel(TimeMixBack b, Chain to) {
+__global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chains_kernel(TimeMixBack b, Chain to) {
   extern __shared__ __align__(16) uint8_t lds[];
   ChunkLds& sh = *(ChunkLds*)lds;
   const bool back = blockIdx.x & 1;
@@ -72,9 +71,9 @@ __global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chains_kernel(T
   if (wave >= 4) {
     if (back) {
       p.v = b.dy;
-      prepare_chunks<T, true, kPreps>(p, begin, end, sh, head, wave - 4, lane);
+      prepare_chunks<T, true>(p, begin, end, sh, head, 4, wave, lane);
     } else {
-      prepare_chunks<T, false, kPreps>(p, begin, end, sh, head, wave - 4, lane);
+      prepare_chunks<T, false>(p, begin, end, sh, head, 4, wave, lane);
     }
     return;
   }
@@ -90,13 +89,13 @@ __global__ void __launch_bounds__(walk_threads(kPreps)) time_mix_chains_kernel(T
   ChunkState st;
   if (!back) {
     st.load(p.state_in ? p.state_in + state : nullptr, wave, lane);
-    walk_chunks<T, 1, false, false>(
-        &st, chunks, sh, wave, lane, [&](int c) { st.store(to.S + (at + (size_t)c * p.heads) * kState, wave, lane); },
+    walk_chunks<T, false, false>(
+        st, chunks, sh, wave, lane, ~0u, [&](int c) { st.store(to.S + (at + (size_t)c * p.heads) * kState, wave, lane); },
         [&](int c, float4v u) { rows(to.U, c, u); }, out);
   } else {
     st.load(b.dstate_out ? b.dstate_out + state : nullptr, wave, lane);
-    walk_chunks<T, 1, false, true>(
-        &st, chunks, sh, wave, lane,
+    walk_chunks<T, false, true>(
+        st, chunks, sh, wave, lane, ~0u,
         [&](int c) { st.store(to.D + (at + (size_t)(chunks - 1 - c) * p.heads) * kState, wave, lane); },
         [&](int c, float4v u) { rows(to.Z, chunks - 1 - c, u); }, out);
     if (b.dstate_in) st.store(b.dstate_in + state, wave, lane);
@@ -433,7 +432,7 @@ hipError_t start_back(const TimeMixBack& b, hipStream_t st) {
   c.D = c.S + n * kState;
   c.U = c.D + n * kState;
   c.Z = c.U + n * kChunk * kHead;
-  hipLaunchKernelGGL(time_mix_chains_kernel<T>, dim3(2u * b.f.seq.nseq * b.f.heads), dim3(walk_threads(kPreps)), sizeof(ChunkLds), st, b,
+  hipLaunchKernelGGL(time_mix_chains_kernel<T>, dim3(2u * b.f.seq.nseq * b.f.heads), dim3(64 * kWalkWaves), sizeof(ChunkLds), st, b,
                      c);
   if (b.f.seq.tokens > 0)
     hipLaunchKernelGGL(time_mix_grad_kernel<T>, dim3((unsigned)n), dim3(256), 0, st, b, c);

@@ -435,7 +435,8 @@ struct ChunkHead {
   uint2 ak[3], v[kV], t[3];
   float4v end[4];
 
-  __device__ __forceinline__ void fetch(const ChunkOps& o, int wave, int lane) {
+  // values: all ones, or 0 to take V for zeros (the map alone)
+  __device__ __forceinline__ void fetch(const ChunkOps& o, int wave, int lane, uint32_t values) {
     const int q = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -444,7 +445,11 @@ struct ChunkHead {
 #pragma unroll
     for (int n = 0; n < 3; ++n) ak[n] = o.ak[n][lane];
 #pragma unroll
-    for (int n = 0; n < kV; ++n) v[n] = rows4(o.v[n], g, q, 16 * wave + 4 * (q & 3));
+    for (int n = 0; n < kV; ++n) {
+      v[n] = rows4(o.v[n], g, q, 16 * wave + 4 * (q & 3));
+      v[n].x &= values;
+      v[n].y &= values;
+    }
 #pragma unroll
     for (int n = 0; n < 3; ++n) t[n] = o.t[n][lane];
     if (REV)
@@ -476,11 +481,10 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-// Takes NS states over a chunk: the first with V, the second, if there is one,
-// without (the map alone).  OUT: Y of the first (row t = 4 g + i, column
-// v = q).  REV: back over it.  save(U) takes U, or Z, as Y is laid out.  x: the
-// states as operands, made again at the end; with REV the states are scaled by
-// the next chunk's `end` before that.
+// Takes the state over a chunk.  OUT: Y (row t = 4 g + i, column v = q).  REV:
+// back over it.  save(U) takes U, or Z, as Y is laid out.  x: the state as
+// operands, made again at the end; with REV the state is scaled by the next
+// chunk's `end` before that.
 //
 // What bounds it: one wave's chain from state to state.  Its products are
 // about 800 cycles of the matrix unit; cutting results into terms and fetching
@@ -489,8 +493,8 @@ __device__ __forceinline__ void interleave() {
 // hand, instruction by instruction: B, K and `end` between the products with A
 // and R, the next chunk's head (`next`) and the cutting of each half of the
 // new state between the products of its update.
-template <typename T, int NS, bool OUT, bool REV, typename Next, typename Save>
-__device__ __forceinline__ float4v chunk_step(ChunkState* st, uint4 (*x)[2][3], const ChunkOps& o, ChunkHead<T, REV>& hd,
+template <typename T, bool OUT, bool REV, typename Next, typename Save>
+__device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], const ChunkOps& o, ChunkHead<T, REV>& hd,
                                               int lane, Next next, Save save) {
   const int q = lane & 15, g = lane >> 4;
   constexpr int NV = ChunkHead<T, REV>::kV;
@@ -517,33 +521,23 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, uint4 (*x)[2][3], 
     }
     if (!REV) end[n] = *(const float4v*)&o.end[ChunkState::channel(n, g)];
   }
-  float4v u0[NS], u1[NS], u[NS], y = zero;
-#pragma unroll
-  for (int m = 0; m < NS; ++m) {
-    u0[m] = mul32<3>(hd.a[0], x[m][0], zero);
-    u1[m] = mul32<3>(hd.a[1], x[m][1], zero);
-    if (m == 0) u1[m] = mul_values<NV>(hd.ak, hd.v, u1[m]);
-  }
+  float4v y = zero;
+  const float4v u0 = mul32<3>(hd.a[0], x[0], zero);
+  float4v u = mul_values<NV>(hd.ak, hd.v, mul32<3>(hd.a[1], x[1], zero));
   if (OUT)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) y = mul32<2>(r[h], x[0][h], y);
-  interleave<(NS * 12 + NV + 1 + (OUT ? 6 : 0)), (OUT || NS == 2 ? 1 : 2), 0>();
+    for (int h = 0; h < 2; ++h) y = mul32<2>(r[h], x[h], y);
+  interleave<(12 + NV + 1 + (OUT ? 6 : 0)), (OUT ? 1 : 2), 0>();
   __builtin_amdgcn_sched_barrier(0);
-  uint2 s[NS][3];
+  uint2 s[3];
+  u += u0;
+  split4<3>(u, s);
+  u = mul_tokens(hd.t, s, zero);
+  split4<3>(u, s);
+  save(u);
+  uint4 uv[3];
 #pragma unroll
-  for (int m = 0; m < NS; ++m) {
-    u[m] = u0[m] + u1[m];
-    split4<3>(u[m], s[m]);
-    u[m] = mul_tokens(hd.t, s[m], zero);
-    split4<3>(u[m], s[m]);
-  }
-  save(u[0]);
-  uint4 uv[NS][3];
-#pragma unroll
-  for (int n = 0; n < 3; ++n) {
-    uv[0][n] = pair(s[0][n], n < NV ? hd.v[n < NV ? n : 0] : make_uint2(0, 0));
-    if (NS > 1) uv[NS - 1][n] = pair(s[NS - 1][n], make_uint2(0, 0));
-  }
+  for (int n = 0; n < 3; ++n) uv[n] = pair(s[n], n < NV ? hd.v[n < NV ? n : 0] : make_uint2(0, 0));
   __builtin_amdgcn_sched_barrier(0);
   next();
   // S' = (S + U^T B + V^T K) diag(end), Y = R S^T + Q (U, V)
@@ -552,28 +546,26 @@ __device__ __forceinline__ float4v chunk_step(ChunkState* st, uint4 (*x)[2][3], 
     uint4 c[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) c[j] = pair(b[n][j], k[n][j]);
-#pragma unroll
-    for (int m = 0; m < NS; ++m) st[m].X[n] = mul32<3>(c, uv[m], st[m].X[n]) * (REV ? hd.end[n] : end[n]);
-    if (n & 1)
-#pragma unroll
-      for (int m = 0; m < NS; ++m) split_half(st[m], n >> 1, x[m][n >> 1]);
+    st.X[n] = mul32<3>(c, uv, st.X[n]) * (REV ? hd.end[n] : end[n]);
+    if (n & 1) split_half(st, n >> 1, x[n >> 1]);
   }
-  if (OUT) y = mul32<2>(qq, uv[0], y);
-  interleave<12 * NS, 1, 0>();
-  interleave<(12 * NS + (OUT ? 3 : 0)), 0, 4>();
+  if (OUT) y = mul32<2>(qq, uv, y);
+  interleave<12, 1, 0>();
+  interleave<(12 + (OUT ? 3 : 0)), 0, 4>();
   __builtin_amdgcn_sched_barrier(0);
   return y;
 }
 
 // A workgroup that walks a run of chunks: waves 0-3 hold the state, sixteen
-// channels of v each, and take it from chunk to chunk; the waves after them
-// prepare the chunks' operands ahead of them, in turn, in LDS buffers.  Two
-// counters per buffer order them: `ready` chunks written, and `done` four per
-// chunk read.  Every wait is for a count that the other side reaches by
+// channels of v each, and take it from chunk to chunk (where the run's map is
+// wanted too, waves 4-7 hold that); the other waves prepare the chunks'
+// operands ahead of them, in turn, in LDS buffers.  Two counters per buffer
+// order them: `ready` chunks written, and `done` one per chunk and walking
+// wave.  Every wait is for a count that the other side reaches by
 // itself: a buffer's chunk c waits for the readers of chunk c - kBuffers, who
 // wait for nothing later than it.
 constexpr int kBuffers = 4;
-constexpr int walk_threads(int preps) { return 64 * (4 + preps); }
+constexpr int kWalkWaves = 12;
 
 struct ChunkLds {
   ChunkOps ops[kBuffers];
@@ -599,13 +591,14 @@ __device__ __forceinline__ void signal(int* count, int lane) {
   asm volatile("" ::: "memory");
 }
 
-// The side of preparing wave `mine`: the chunks of tokens begin..end, from the
-// last to the first with REV.
-template <typename T, bool REV, int PREPS>
-__device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int end, ChunkLds& sh, int head, int mine, int lane) {
+// The side of preparing wave `wave`, which comes after `walkers` others: the
+// chunks of tokens begin..end, from the last to the first with REV.
+template <typename T, bool REV>
+__device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int end, ChunkLds& sh, int head, int walkers, int wave,
+                                               int lane) {
   const int chunks = (end - begin + kChunk - 1) / kChunk;
   ChunkPrep<T, REV> prep;
-  for (int c = mine; c < chunks; c += PREPS) {
+  for (int c = wave - walkers; c < chunks; c += kWalkWaves - walkers) {
     ChunkOps& o = sh.ops[c % kBuffers];
     const int t = begin + (REV ? chunks - 1 - c : c) * kChunk;
     prep.load(p, head, t, min(kChunk, end - t), lane);
@@ -616,7 +609,7 @@ __device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int 
     __builtin_amdgcn_sched_barrier(0);
     prep.grams();
     __builtin_amdgcn_sched_barrier(0);
-    wait_for(&sh.done[c % kBuffers], c / kBuffers * 4);
+    wait_for(&sh.done[c % kBuffers], c / kBuffers * walkers);
     prep.put_rows(o, lane);
     __builtin_amdgcn_sched_barrier(0);
     prep.solve(o, lane);
@@ -624,24 +617,22 @@ __device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int 
   }
 }
 
-// The state's waves' side: NS states (see chunk_step) over the run.  In the
-// c-th chunk of the walk: before(c) with the state at hand (multiplied by
-// `end` with REV), save(c, U or Z), and out(c, Y) with OUT.
-template <typename T, int NS, bool OUT, bool REV, typename Before, typename Save, typename Out>
-__device__ __forceinline__ void walk_chunks(ChunkState* st, int chunks, ChunkLds& sh, int wave, int lane, Before before,
-                                            Save save, Out out) {
+// A walking wave's side: its part of a state over the run, or of the map
+// (values 0).  In the c-th chunk of the walk: before(c) with the state at hand
+// (multiplied by `end` with REV), save(c, U or Z), and out(c, Y) with OUT.
+template <typename T, bool OUT, bool REV, typename Before, typename Save, typename Out>
+__device__ __forceinline__ void walk_chunks(ChunkState& st, int chunks, ChunkLds& sh, int wave, int lane, uint32_t values,
+                                            Before before, Save save, Out out) {
   ChunkHead<T, REV> hd;
-  uint4 x[NS][2][3];
+  uint4 x[2][3];
   if (chunks > 0) {
     wait_for(&sh.ready[0], 1);
-    hd.fetch(sh.ops[0], wave, lane);
+    hd.fetch(sh.ops[0], wave, lane, values);
     if (REV)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) st[0].X[n] *= hd.end[n];
+      for (int n = 0; n < 4; ++n) st.X[n] *= hd.end[n];
 #pragma unroll
-    for (int m = 0; m < NS; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) split_half(st[m], h, x[m][h]);
+    for (int h = 0; h < 2; ++h) split_half(st, h, x[h]);
   }
   for (int c = 0; c < chunks; ++c) {
     const int n = c + 1;
@@ -649,14 +640,14 @@ __device__ __forceinline__ void walk_chunks(ChunkState* st, int chunks, ChunkLds
     before(c);
     // looked at early, so that the answer is here when it is needed
     const int seen = __hip_atomic_load(&sh.ready[n % kBuffers], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-    const float4v y = chunk_step<T, NS, OUT, REV>(
+    const float4v y = chunk_step<T, OUT, REV>(
         st, x, o, hd, lane,
         [&] {
           const int want = n < chunks ? n / kBuffers + 1 : 0;
           if (__builtin_amdgcn_readfirstlane(seen) < want) wait_for(&sh.ready[n % kBuffers], want);
           asm volatile("" ::: "memory");
           // (past the last chunk whatever the buffer holds, for nothing)
-          hd.fetch(sh.ops[n % kBuffers], wave, lane);
+          hd.fetch(sh.ops[n % kBuffers], wave, lane, values);
           if (REV && n >= chunks)
 #pragma unroll
             for (int i = 0; i < 4; ++i) hd.end[i] = float4v{1.f, 1.f, 1.f, 1.f};
