@@ -6,7 +6,8 @@
 // with mean and variance over a head's 64 channels.  One pass over five rows
 // in and one out (backward: six and five); eight lanes hold a head, eight
 // channels each, so the three sums are three lane exchanges and nothing goes
-// through LDS.  Bound by memory.
+// through LDS.  Bound by memory: 8192 tokens of width 2560 take 50 us, 5.0 TB/s,
+// what a copy reaches; 32 tokens of width 4096 2.6 us, a launch.
 #include "mix.h"
 
 namespace rq {
@@ -67,7 +68,8 @@ hipError_t launch_head_gate(const HeadGate& p, bool bf16, hipStream_t st) {
 // A wave covers 512 channels, the workgroup's four waves every fourth of its
 // rows; the parameter gradients stay in registers, are added across the waves
 // in LDS and written as one row of partial sums per workgroup, so their order
-// is fixed.
+// is fixed.  Bound by memory: 4096 tokens of width 2048 in bf16 take 39 to 44
+// us, 4.2 to 4.7 TB/s, and the sums of the partial rows 5 us more.
 template <typename T>
 __global__ void __launch_bounds__(256) head_gate_back_kernel(HeadGateBack b, int rows) {
   const HeadGate& p = b.f;

@@ -11,7 +11,9 @@
 // A workgroup owns a run of consecutive rows and holds a row in registers,
 // several channels per thread; h of the row before stays in registers
 // from one row to the next and is computed again where a run begins inside a
-// sequence.
+// sequence.  Measured with six mixtures: 4099 tokens of width 2560 in bf16 45
+// us, 4.2 TB/s (a copy reaches 5.0); 32 tokens of width 4096 5.7 us, of which
+// half is the launch and the rest one row's chain: offsets, slot, row, two sums.
 #include "mix.h"
 
 namespace rq {
@@ -265,7 +267,9 @@ int threads_of(int width, int nv) { return (width / 8 + nv * 64 - 1) / (nv * 64)
 hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
   const int nv = p.width > 4096 ? 2 : 1;
   // one row per workgroup while the rows do not fill the card, then four (a
-  // run's first row costs the norm of the row before it)
+  // run's first row costs the norm of the row before it; 4099 rows of width 2560
+  // take 51 us by twos, 48.5 by fours, 47.5 by eights, of which few rows leave
+  // compute units idle)
   const int rows = p.seq.tokens <= 1024 ? 1 : 4 + p.seq.tokens / (1 << 22);
   const int tiles = (p.seq.tokens + rows - 1) / rows;
   const int empty = p.shift_out && (p.seq.cu || p.seq.tokens == 0) && p.shift_out != p.shift_in ? p.seq.nseq : 0;
@@ -294,7 +298,9 @@ hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
 // the sums of eight parameters' gradients and three rows take most of the 128
 // registers that a workgroup of 1024 has.  The parameter gradients stay in
 // registers over the run and are written as one row of partial sums, which a
-// second kernel adds in order.
+// second kernel adds in order.  Measured: 4096 tokens of width 2048, six
+// mixtures, bf16, 64 us, 2.6 TB/s: two workgroups per compute unit do not hide
+// each row's barrier and sums, and their registers allow no third.
 template <typename T, int NV, int NM>
 __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, int rows, bool mu_lds) {
   extern __shared__ __align__(16) float mus[];  // mu, if it fits: each row needs all of it
@@ -545,7 +551,9 @@ hipError_t start_back(const ShiftNormBack& p, int rows, dim3 grid, dim3 block, h
 hipError_t launch_shift_norm_back(const ShiftNormBack& p, bool bf16, hipStream_t st) {
   const int nv = p.width > 4096 ? 2 : 1;
   const size_t row = (size_t)(2 + p.nmix) * p.width * 4;
-  int64_t groups = 512;  // two workgroups per compute unit
+  // two workgroups per compute unit (with the sums after it 70 us for 4096
+  // tokens of width 2048; 256 workgroups 71, 768 97, 1024 90)
+  int64_t groups = 512;
   const int64_t fit = p.parts ? (int64_t)(p.parts_bytes / row) : 0;
   if (groups > fit) groups = fit;
   if (groups > p.seq.tokens) groups = p.seq.tokens;

@@ -8,7 +8,12 @@
 // token in fp32.  The rows of S are independent of each other, so a wave owns
 // sixteen of them; a row lies across sixteen lanes, four columns each, and the
 // sums S a and S r are four lane rotations.  A run of up to sixteen tokens is
-// staged in LDS as fp32.
+// staged in LDS as fp32.  For single tokens the states' bytes bound it: 32
+// sequences of 64 heads take 13 us, 5.1 TB/s, what a copy reaches.  For longer
+// ones the chain from token to token does, 0.4 us each.
+//
+// chunk kernel: one workgroup of twelve waves per (sequence or segment, head),
+// sixteen tokens at a time on matrix instructions (time_mix_chunk.h).
 #include <climits>
 
 #include "mix.h"

@@ -54,6 +54,10 @@ struct Chain {
 };
 }  // namespace
 
+// A workgroup per sequence, head and direction.  Bound by the walk's chain and,
+// where all compute units have one, by what it writes: 4 sequences of 1024
+// tokens and 32 heads take 126 us, without writing the states 94.  Keeping them
+// for every second chunk only (107 us) costs the second launch more.
 template <typename T>
 __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chains_kernel(TimeMixBack b, Chain to) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -169,7 +173,9 @@ __device__ __forceinline__ float entry(const uint4* t, int half, int i) {
 }  // namespace
 
 // The gradients of one chunk and head: four waves, of which wave w takes
-// channels 16 w .. 16 w + 15.
+// channels 16 w .. 16 w + 15.  Bound by memory: for 4 sequences of 1024 tokens
+// and 32 heads it reads the 335 MB that the chains leave and moves 220 MB of
+// rows, in 132 us, 4.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Chain from) {
   __shared__ __align__(16) GradLds sh;

@@ -492,7 +492,9 @@ __device__ __forceinline__ void interleave() {
 // wave's issue and no more than fifteen in flight.  So the three are mixed by
 // hand, instruction by instruction: B, K and `end` between the products with A
 // and R, the next chunk's head (`next`) and the cutting of each half of the
-// new state between the products of its update.
+// new state between the products of its update.  Measured: 0.91 us a chunk by
+// itself, 1.1 beside the preparing waves (which take 0.65 by themselves), 1.3
+// with every compute unit at work, when the clock falls.
 template <typename T, bool OUT, bool REV, typename Next, typename Save>
 __device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], const ChunkOps& o, ChunkHead<T, REV>& hd,
                                               int lane, Next next, Save save) {
