@@ -266,11 +266,13 @@ int threads_of(int width, int nv) { return (width / 8 + nv * 64 - 1) / (nv * 64)
 
 hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
   const int nv = p.width > 4096 ? 2 : 1;
-  // one row per workgroup while the rows do not fill the card, then four (a
-  // run's first row costs the norm of the row before it; 4099 rows of width 2560
-  // take 51 us by twos, 48.5 by fours, 47.5 by eights, of which few rows leave
-  // compute units idle)
-  const int rows = p.seq.tokens <= 1024 ? 1 : 4 + p.seq.tokens / (1 << 22);
+  // A run's first row costs the norm of the row before it, a long one leaves
+  // compute units idle.  Rows one, two, four, eight at a time, in us, at width
+  // 2048 with six mixtures and at width 2560 with one: 600 rows 9.7 10.8 14 22
+  // and 7.7 7.6 9.1 13; 1025 rows 12.8 12.9 16 24 and 11 8.7 10 14; 2048 rows 22
+  // 18 19 27 and 20 16 14 16; 4099 rows 42 35 35 38 and 34 27 25 23; 16384 rows
+  // 139 134 132 153 and 117 86 77 78.
+  const int rows = p.seq.tokens <= 768 ? 1 : p.seq.tokens <= 1536 ? 2 : 4 + p.seq.tokens / (1 << 22);
   const int tiles = (p.seq.tokens + rows - 1) / rows;
   const int empty = p.shift_out && (p.seq.cu || p.seq.tokens == 0) && p.shift_out != p.shift_in ? p.seq.nseq : 0;
   if (tiles + empty == 0) return hipSuccess;

@@ -280,7 +280,7 @@ def test_slots_outside_the_array():
     assert torch.equal(new[1], shift[1])
 
 
-NORM_LENS = [[1], [5], [0, 3, 0, 1, 9, 0], [1] * 32, [37], [700, 0, 600]]
+NORM_LENS = [[1], [5], [0, 3, 0, 1, 9, 0], [1] * 32, [37], [700, 0, 600], [900, 0, 801]]
 
 
 @pytest.mark.parametrize("code", TYPES, ids=IDS)
