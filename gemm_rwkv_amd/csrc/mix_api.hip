@@ -57,11 +57,12 @@ struct Buffers {
     out[nout++] = bytes_span(p, n);
   }
   // 16-bit rows [m][ld], n used per row
+  // no rows may be no array: an empty tensor's address is null
   void read_rows(const void* p, int64_t m, int64_t n, int64_t ld, bool needed = true) {
-    if (pointer(p, needed)) in[nin++] = rqv::act_span(p, m, n, ld, 2);
+    if (pointer(p, needed && m > 0)) in[nin++] = rqv::act_span(p, m, n, ld, 2);
   }
   void write_rows(const void* p, int64_t m, int64_t n, int64_t ld, bool needed = true) {
-    if (!pointer(p, needed)) return;
+    if (!pointer(p, needed && m > 0)) return;
     same[nout] = nullptr;
     out[nout++] = rqv::act_span(p, m, n, ld, 2);
   }

@@ -392,7 +392,8 @@ int rq_gemm_int8_acc(const int8_t *xq, int64_t m, const rq_qweight *w, int32_t *
  * fp32; every sum, statistic and state is held in fp32 or more.
  *
  * Rows.  An activation is [tokens][ld] with ld >= the width and ld % 8 == 0
- * (RQ_ERR_ALIGN), tokens counted over all sequences.
+ * (RQ_ERR_ALIGN), tokens counted over all sequences.  With no tokens the
+ * arrays of rows may be NULL.
  *
  * Sequences.  The rows of nseq sequences follow one another.  cu (device,
  * int32, 4-byte aligned) holds their nseq + 1 offsets, cu[0] = 0,

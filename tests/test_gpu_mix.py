@@ -393,12 +393,14 @@ def test_head_of_equal_values():
     close(out.get(), mix.head_gate(y[1], *(one[1],) * 4, o, o, 64e-5, o), code, "out")
 
 
-def test_no_tokens():
-    """Empty calls carry states over and clear the parameters' gradients."""
+@pytest.mark.parametrize("rows_held", [8, 0], ids=["arrays", "null"])
+def test_no_tokens(rows_held):
+    """Empty calls carry states over and clear the parameters' gradients, also
+    with the null addresses of empty tensors."""
     code, c = rq.RQ_BF16, 64
-    say("no tokens")
+    say("no tokens", rows_held)
     f32 = dict(dtype=torch.float32, device="cuda")
-    e = torch.empty(8, c, dtype=torch.bfloat16, device="cuda")
+    e = torch.empty(rows_held, c, dtype=torch.bfloat16, device="cuda")
     more = [torch.empty_like(e) for _ in range(6)]
     st, so = torch.randn(2, 1, 64, 64, **f32), torch.empty(2, 1, 64, 64, **f32)
     rq.rq_time_mix(code, *(e,) * 6, 0, 1, c, None, 2, st, so, None, 2, more[0], c)
