@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chunk_kernel(TimeMix
   if (!find_segment(p.seq, split, idx, sg) || sg.end - sg.begin <= over || (sg.nth == 0 && sg.of > 1)) return;
   clear_counts(sh);
   if (wave >= 4) {
-    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, 4, wave, lane);
+    prepare_chunks<T, true, false>(p, sg.begin, sg.end, sh, head, 4, wave, lane);
     return;
   }
   const int slot = slot_of(p.slots, sg.seq);
@@ -219,7 +219,10 @@ __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_segment_kernel(TimeM
   clear_counts(sh);
   const int walkers = sg.nth ? 8 : 4;  // the state, and the map
   if (wave >= walkers) {
-    prepare_chunks<T, false>(p, sg.begin, sg.end, sh, head, walkers, wave, lane);
+    if (sg.nth == 0)
+      prepare_chunks<T, true, false>(p, sg.begin, sg.end, sh, head, walkers, wave, lane);
+    else
+      prepare_chunks<T, false, false>(p, sg.begin, sg.end, sh, head, walkers, wave, lane);
     return;
   }
   float* to = split.states + ((size_t)idx * p.heads + head) * 2 * kHead * kHead;

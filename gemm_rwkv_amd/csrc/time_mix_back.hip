@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chains_kernel(TimeMi
   if (wave >= 4) {
     if (back) {
       p.v = b.dy;
-      prepare_chunks<T, true>(p, begin, end, sh, head, 4, wave, lane);
+      prepare_chunks<T, false, true>(p, begin, end, sh, head, 4, wave, lane);
     } else {
-      prepare_chunks<T, false>(p, begin, end, sh, head, 4, wave, lane);
+      prepare_chunks<T, false, false>(p, begin, end, sh, head, 4, wave, lane);
     }
     return;
   }

@@ -14,8 +14,8 @@
 // Precision.  A matrix instruction multiplies bf16 exactly and adds in fp32,
 // so an fp32 factor is cut into three bf16 terms that hold its 24 bits
 // exactly, and a product of two such factors keeps the six term products
-// above 2^-24 of it: what feeds the state is as exact as fp32.  Y, which is
-// rounded to 16 bits, takes two terms and three products (2^-16).
+// above 2^-24 of it: states and outputs are as exact as fp32 before an output
+// is rounded.
 //
 // Lanes.  l = 16 g + q.  A 16x16 result has row 4 g + i in register i and
 // column q.  As the B operand of the next product, its registers are the
@@ -81,15 +81,11 @@ __device__ __forceinline__ void split4(float4v x, uint2* t) {
   for (int n = 0; n < NT; ++n) t[n] = make_uint2(w[0][n], w[1][n]);
 }
 
-// The term products that count, smallest first: of three terms the six above
-// 2^-24, of two the three above 2^-16.
-template <int NT>
+// The term products that count, smallest first: the six above 2^-24.
 __device__ __forceinline__ float4v mul32(const uint4* a, const uint4* b, float4v c) {
-  if (NT == 3) {
-    c = mfma32(a[0], b[2], c);
-    c = mfma32(a[2], b[0], c);
-    c = mfma32(a[1], b[1], c);
-  }
+  c = mfma32(a[0], b[2], c);
+  c = mfma32(a[2], b[0], c);
+  c = mfma32(a[1], b[1], c);
   c = mfma32(a[0], b[1], c);
   c = mfma32(a[1], b[0], c);
   return mfma32(a[0], b[0], c);
@@ -118,8 +114,8 @@ __device__ __forceinline__ float4v mul_values(const uint2* a, const uint2* b, fl
 // hold the state.
 struct ChunkOps {
   uint4 a[3][2][64];    // A: terms, channel halves, lanes (row q, channels 32 h + 8 g + j)
-  uint4 r[2][2][64];    // R, two terms (forward only, as q)
-  uint4 q[2][64];       // row q, slots j < 4: Qb at 4 g + j, j >= 4: Qk
+  uint4 r[3][2][64];    // R (where Y is wanted, as q)
+  uint4 q[3][64];       // row q, slots j < 4: Qb at 4 g + j, j >= 4: Qk
   uint2 t[3][64];       // T: row q, slots 4 g + i
   uint2 ak[3][64];      // Ak: row q, slots 4 g + i
   uint4 b[3][16 * 8];   // B rows [16][64 channels] in blocks of eight, see row_block
@@ -163,24 +159,30 @@ __device__ __forceinline__ float dpp_or(float old, float v) {
 //   Z = T^T (B D^T + Qb^T dY),   dS = D + Z^T A + dY^T R
 // which is the forward chain with B for A, Qb^T for Ak, T^T for T, A and R for
 // B and K, and dY for V (p.v is dY then, and p.k is not read).
-template <typename T, bool REV = false>
+//
+// OUT: with what Y takes, R, Qb and Qk.
+template <typename T, bool OUT, bool REV>
 struct ChunkPrep {
-  static constexpr int kR = REV ? 3 : 2;  // terms of R
   uint4 raw[6][2];  // r, w, k, v, a, b
-  float fall[16], grow[16], before[16];
-  uint4 at[3][2], rt[kR][2], bt[3][2], kt[3][2];
+  float fall[16], grow[16];
+  uint4 at[3][2], rt[3][2], bt[3][2], kt[3][2];
   float4v ab, ak, qb, qk;
 
   __device__ __forceinline__ void load(const TimeMix& p, int head, int t0, int n, int lane) {
     const int q = lane & 15, g = lane >> 4;
     const bool held = q < n;
-    const size_t at0 = (size_t)(t0 + q) * p.ld + head * kHead + 8 * g;
+    // one address for the wave per array, one offset per lane for all; made
+    // anew for each chunk, because six lane addresses kept would cost twelve
+    // registers, which spill
+    const size_t row = (size_t)t0 * p.ld + head * kHead;
+    size_t at0 = (size_t)q * p.ld + 8 * g;
+    asm volatile("" : "+v"(at0));
     const void* src[6] = {p.r, p.w, p.k, p.v, p.a, p.b};
 #pragma unroll
     for (int i = 0; i < 6; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (!REV || i != 2) raw[i][h] = block_or(i == 1 ? T::kMinusInf2 : 0u, src[i], at0 + 32 * h, held);
+        if ((OUT || REV || i != 0) && (!REV || i != 2)) raw[i][h] = block_or(i == 1 ? T::kMinusInf2 : 0u, (const uint16_t*)src[i] + row, at0 + 32 * h, held);
   }
 
   __device__ __forceinline__ static void up8(uint4 v, float* f) {
@@ -190,8 +192,7 @@ struct ChunkPrep {
     up2<T>(v.w, f + 6);
   }
 
-  // accumulated decays: a sum over the 16 lanes of a row, then 2^L, 2^-L and
-  // the row before's 2^L
+  // accumulated decays: a sum over the 16 lanes of a row, then 2^L and 2^-L
   __device__ __forceinline__ void decays() {
     float w[16];
     up8(raw[1][0], w);
@@ -205,7 +206,6 @@ struct ChunkPrep {
       l += dpp<0x118>(l);
       fall[j] = __builtin_amdgcn_exp2f(l);
       grow[j] = __builtin_amdgcn_exp2f(-l);
-      before[j] = dpp_or<0x111>(1.f, fall[j]);
     }
   }
 
@@ -213,56 +213,55 @@ struct ChunkPrep {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 t[3];
-      float x[8];
+      float x[8], before[8];  // 2^L of the row before
+#pragma unroll
+      for (int j = 0; j < 8; ++j) before[j] = dpp_or<0x111>(1.f, fall[8 * h + j]);
       auto scaled = [&](int which, const float* s) {
         up8(raw[which][h], x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= s[8 * h + j];
+        for (int j = 0; j < 8; ++j) x[j] *= s[j];
       };
       scaled(4, before);
       split8<3>(x, t);
       at[0][h] = t[0]; at[1][h] = t[1]; at[2][h] = t[2];
-      scaled(5, grow);
+      scaled(5, grow + 8 * h);
       split8<3>(x, t);
       bt[0][h] = t[0]; bt[1][h] = t[1]; bt[2][h] = t[2];
       if (!REV) {
-        scaled(2, grow);
+        scaled(2, grow + 8 * h);
         split8<3>(x, t);
         kt[0][h] = t[0]; kt[1][h] = t[1]; kt[2][h] = t[2];
       }
-      scaled(0, fall);
-      split8<kR>(x, t);
-#pragma unroll
-      for (int n = 0; n < kR; ++n) rt[n][h] = t[n];
+      if (OUT || REV) {
+        scaled(0, fall + 8 * h);
+        split8<3>(x, t);
+        rt[0][h] = t[0]; rt[1][h] = t[1]; rt[2][h] = t[2];
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   // X Y^T over the 64 channels
-  template <int NT, int NX, int NY>
-  __device__ __forceinline__ static float4v gram(const uint4 (&x)[NX][2], const uint4 (&y)[NY][2]) {
+  __device__ __forceinline__ static float4v gram(const uint4 (&x)[3][2], const uint4 (&y)[3][2]) {
     float4v c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint4 a[NT], b[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        a[n] = x[n][h];
-        b[n] = y[n][h];
-      }
-      c = mul32<NT>(a, b, c);
+      const uint4 a[3] = {x[0][h], x[1][h], x[2][h]}, b[3] = {y[0][h], y[1][h], y[2][h]};
+      c = mul32(a, b, c);
     }
     return c;
   }
 
   __device__ __forceinline__ void grams() {
-    ab = gram<3>(at, bt);  // row t = 4 g + i, column s = q
+    ab = gram(at, bt);  // row t = 4 g + i, column s = q
     if (REV) {
-      ak = gram<3>(rt, bt);  // row t = 4 g + i, column s = q: the operand of Qb^T
+      ak = gram(rt, bt);  // row t = 4 g + i, column s = q: the operand of Qb^T
       return;
     }
-    ak = gram<3>(kt, at);  // row s = 4 g + i, column t = q: already the operand of Ak
-    qb = gram<2>(bt, rt);
-    qk = gram<2>(kt, rt);
+    ak = gram(kt, at);  // row s = 4 g + i, column t = q: already the operand of Ak
+    if (!OUT) return;
+    qb = gram(bt, rt);
+    qk = gram(kt, rt);
   }
 
   __device__ __forceinline__ void put_rows(ChunkOps& o, int lane) const {
@@ -274,11 +273,8 @@ struct ChunkPrep {
       for (int n = 0; n < 3; ++n) {
         o.a[n][h][lane] = REV ? bt[n][h] : at[n][h];
         o.b[n][block] = REV ? at[n][h] : bt[n][h];
-        o.k[n][block] = REV ? rt[n < kR ? n : 0][h] : kt[n][h];
-      }
-      if (!REV) {
-        o.r[0][h][lane] = rt[0][h];
-        o.r[1][h][lane] = rt[1][h];
+        o.k[n][block] = REV ? rt[n][h] : kt[n][h];
+        if (OUT) o.r[n][h][lane] = rt[n][h];
       }
       put_v(o, block, raw[3][h], (T*)nullptr);
       if (q == 15)
@@ -360,22 +356,23 @@ struct ChunkPrep {
 #pragma unroll
     for (int n = 0; n < 3; ++n) o.t[n][lane] = t[n];
     // slot s = 4 g + i of row t = q
-    float4v k = ak, qbm = qb, qkm = qk;
+    float4v k = ak;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = 4 * g + i;
-      if (REV ? s < q : s >= q) k[i] = 0.f;
-      if (s > q) qbm[i] = qkm[i] = 0.f;
-    }
+    for (int i = 0; i < 4; ++i)
+      if (REV ? 4 * g + i < q : 4 * g + i >= q) k[i] = 0.f;
     split4<3>(k, t);
 #pragma unroll
     for (int n = 0; n < 3; ++n) o.ak[n][lane] = t[n];
-    if (REV) return;
-    uint2 b[2], c[2];
-    split4<2>(qbm, b);
-    split4<2>(qkm, c);
+    if (!OUT) return;
+    float4v qbm = qb, qkm = qk;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) o.q[n][lane] = make_uint4(b[n].x, b[n].y, c[n].x, c[n].y);
+    for (int i = 0; i < 4; ++i)
+      if (4 * g + i > q) qbm[i] = qkm[i] = 0.f;
+    uint2 b[3], c[3];
+    split4<3>(qbm, b);
+    split4<3>(qkm, c);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) o.q[n][lane] = make_uint4(b[n].x, b[n].y, c[n].x, c[n].y);
   }
 };
 
@@ -501,14 +498,14 @@ __device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], con
   const int q = lane & 15, g = lane >> 4;
   constexpr int NV = ChunkHead<T, REV>::kV;
   const float4v zero = {0.f, 0.f, 0.f, 0.f};
-  uint4 r[2][2], qq[2];
+  uint4 r[2][3], qq[3];
   if (OUT) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) r[h][n] = o.r[n][h][lane];
+      for (int n = 0; n < 3; ++n) r[h][n] = o.r[n][h][lane];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) qq[n] = o.q[n][lane];
+    for (int n = 0; n < 3; ++n) qq[n] = o.q[n][lane];
   }
   __builtin_amdgcn_sched_barrier(0);
   // A S^T + Ak V, R S^T
@@ -524,12 +521,12 @@ __device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], con
     if (!REV) end[n] = *(const float4v*)&o.end[ChunkState::channel(n, g)];
   }
   float4v y = zero;
-  const float4v u0 = mul32<3>(hd.a[0], x[0], zero);
-  float4v u = mul_values<NV>(hd.ak, hd.v, mul32<3>(hd.a[1], x[1], zero));
+  const float4v u0 = mul32(hd.a[0], x[0], zero);
+  float4v u = mul_values<NV>(hd.ak, hd.v, mul32(hd.a[1], x[1], zero));
   if (OUT)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) y = mul32<2>(r[h], x[h], y);
-  interleave<(12 + NV + 1 + (OUT ? 6 : 0)), (OUT ? 1 : 2), 0>();
+    for (int h = 0; h < 2; ++h) y = mul32(r[h], x[h], y);
+  interleave<(12 + NV + 1 + (OUT ? 12 : 0)), (OUT ? 1 : 2), 0>();
   __builtin_amdgcn_sched_barrier(0);
   uint2 s[3];
   u += u0;
@@ -548,12 +545,12 @@ __device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], con
     uint4 c[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) c[j] = pair(b[n][j], k[n][j]);
-    st.X[n] = mul32<3>(c, uv, st.X[n]) * (REV ? hd.end[n] : end[n]);
+    st.X[n] = mul32(c, uv, st.X[n]) * (REV ? hd.end[n] : end[n]);
     if (n & 1) split_half(st, n >> 1, x[n >> 1]);
   }
-  if (OUT) y = mul32<2>(qq, uv, y);
+  if (OUT) y = mul32(qq, uv, y);
   interleave<12, 1, 0>();
-  interleave<(12 + (OUT ? 3 : 0)), 0, 4>();
+  interleave<(12 + (OUT ? 6 : 0)), 0, 4>();
   __builtin_amdgcn_sched_barrier(0);
   return y;
 }
@@ -595,11 +592,11 @@ __device__ __forceinline__ void signal(int* count, int lane) {
 
 // The side of preparing wave `wave`, which comes after `walkers` others: the
 // chunks of tokens begin..end, from the last to the first with REV.
-template <typename T, bool REV>
+template <typename T, bool OUT, bool REV>
 __device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int end, ChunkLds& sh, int head, int walkers, int wave,
                                                int lane) {
   const int chunks = (end - begin + kChunk - 1) / kChunk;
-  ChunkPrep<T, REV> prep;
+  ChunkPrep<T, OUT, REV> prep;
   for (int c = wave - walkers; c < chunks; c += kWalkWaves - walkers) {
     ChunkOps& o = sh.ops[c % kBuffers];
     const int t = begin + (REV ? chunks - 1 - c : c) * kChunk;
