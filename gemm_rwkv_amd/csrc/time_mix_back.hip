@@ -110,23 +110,29 @@ namespace {
 constexpr int kPad = 68;  // floats of a row of decays: 16-byte writes of 16 rows spread over the banks
 
 // Operands of a chunk's gradients: rows [16][64] in blocks of eight channels
-// (row_block), two bf16 terms, and the 16x16 matrices as operands.
+// (row_block) and the 16x16 matrices as operands, in bf16 terms: three for
+// fp32 values, NV for V and dY, which those hold exactly.
+template <int NV>
 struct GradLds {
-  uint4 a[2][128], r[2][128], b[2][128], k[2][128], u[2][128], z[2][128], dy[2][128], v[2][128];
+  uint4 a[3][128], r[3][128], b[3][128], k[3][128], u[3][128], z[3][128], dy[NV][128], v[NV][128];
   float fall[kChunk][kPad], sig[kChunk][kPad];
   float diag[2][kChunk];  // of dQb and dQk, which are without it below
-  uint4 mr[2][64];  // (dQb, dQk), two terms
-  uint4 ma[2][64];  // (dAb, dAk)
-  uint4 mb[2][64];  // (dQb^T, dAb^T)
-  uint4 mk[2][64];  // (dQk^T, dAk^T)
-  uint4 mv[2][64];  // (Qk^T, Ak^T)
+  uint4 mr[3][64];  // (dQb, dQk)
+  uint4 ma[3][64];  // (dAb, dAk)
+  uint4 mb[3][64];  // (dQb^T, dAb^T)
+  uint4 mk[3][64];  // (dQk^T, dAk^T)
+  uint4 mv[3][64];  // (Qk^T, Ak^T)
 };
 
+// The term products that count, smallest first: those above 2^-24.
 template <int NA, int NB>
 __device__ __forceinline__ float4v mul_terms(const uint4* a, const uint4* b, float4v c) {
-  if (NB > 1) c = mfma32(a[0], b[NB - 1], c);
-  if (NA > 1) c = mfma32(a[NA - 1], b[0], c);
-  return mfma32(a[0], b[0], c);
+#pragma unroll
+  for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (sum - i >= 0 && sum - i < NB) c = mfma32(a[i], b[sum - i], c);
+  return c;
 }
 
 // X Y^T over the 64 channels of two rows' worth of operands in LDS: row 4 g + i
@@ -154,17 +160,17 @@ __device__ __forceinline__ void put_half(uint4 (*m)[64], int half, float4v x, in
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (!keep(4 * g + i - q)) x[i] = 0.f;
-  uint2 t[2];
-  split4<2>(x, t);
+  uint2 t[3];
+  split4<3>(x, t);
 #pragma unroll
-  for (int n = 0; n < 2; ++n) ((uint2*)&m[n][lane])[half] = t[n];
+  for (int n = 0; n < 3; ++n) ((uint2*)&m[n][lane])[half] = t[n];
 }
 
-// Entry i of four rows of a two-term operand half (x, y words).
+// Entry i of four rows of an operand half (x, y words).
 __device__ __forceinline__ float entry(const uint4* t, int half, int i) {
   float s = 0.f;
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
+  for (int n = 0; n < 3; ++n) {
     const uint32_t w = half ? (i < 2 ? t[n].z : t[n].w) : (i < 2 ? t[n].x : t[n].y);
     s += BF16::up((i & 1) ? w >> 16 : w & 0xffffu);
   }
@@ -177,10 +183,10 @@ __device__ __forceinline__ float entry(const uint4* t, int half, int i) {
 // and 32 heads it reads the 335 MB that the chains leave and moves 220 MB of
 // rows, in 132 us, 4.2 TB/s.
 template <typename T>
-__global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Chain from) {
-  __shared__ __align__(16) GradLds sh;
-  const TimeMix& p = b.f;
+__global__ void __launch_bounds__(256, 2) time_mix_grad_kernel(TimeMixBack b, Chain from) {
   constexpr int NV = ChunkHead<T, false>::kV;
+  __shared__ __align__(16) GradLds<NV> sh;
+  const TimeMix& p = b.f;
   const int head = blockIdx.x % p.heads, j = blockIdx.x / p.heads;
   int begin, end, c;
   if (!find_chunk(p.seq, j, begin, end, c)) return;
@@ -236,22 +242,22 @@ __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Ch
     *(float4v*)&sh.fall[q][16 * wave + 4 * g] = float4v{fall[0], fall[1], fall[2], fall[3]};
     *(float4v*)&sh.sig[q][16 * wave + 4 * g] = float4v{sig[0], sig[1], sig[2], sig[3]};
     const int block = row_block(q, 2 * wave + (g >> 1)), half = g & 1;
-    auto put2 = [&](uint4(*m)[128], float4v f) {
-      uint2 t[2];
-      split4<2>(f, t);
+    auto put3 = [&](uint4(*m)[128], float4v f) {
+      uint2 t[3];
+      split4<3>(f, t);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ((uint2*)&m[i][block])[half] = t[i];
+      for (int i = 0; i < 3; ++i) ((uint2*)&m[i][block])[half] = t[i];
     };
     auto put_scaled = [&](uint4(*m)[128], int i, const float* s) {
       up4(i);
-      put2(m, float4v{x[0] * s[0], x[1] * s[1], x[2] * s[2], x[3] * s[3]});
+      put3(m, float4v{x[0] * s[0], x[1] * s[1], x[2] * s[2], x[3] * s[3]});
     };
     put_scaled(sh.r, 0, fall);
     put_scaled(sh.k, 2, grow);
     put_scaled(sh.a, 3, before);
     put_scaled(sh.b, 4, grow);
-    put2(sh.u, u);
-    put2(sh.z, z);
+    put3(sh.u, u);
+    put3(sh.z, z);
 #pragma unroll
     for (int i = 5; i < 7; ++i) {
       uint4(*m)[128] = i == 5 ? sh.v : sh.dy;
@@ -259,7 +265,10 @@ __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Ch
         ((uint2*)&m[0][block])[half] = raw[i];
       } else {
         up4(i);
-        put2(m, float4v{x[0], x[1], x[2], x[3]});
+        uint2 t[2];
+        split4<2>(float4v{x[0], x[1], x[2], x[3]}, t);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) ((uint2*)&m[n][block])[half] = t[n];
       }
     }
   }
@@ -275,23 +284,23 @@ __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Ch
       if (4 * g + i == q) to[q] = x[i];
   };
   if (wave == 0) {
-    const float4v x = gram_rows<2, NV>(sh.u, sh.dy, q, g);
+    const float4v x = gram_rows<3, NV>(sh.u, sh.dy, q, g);
     put_diag(sh.diag[0], x);
     put_half(sh.mr, 0, x, q, g, lane, strict);
-    put_half(sh.mb, 0, gram_rows<NV, 2>(sh.dy, sh.u, q, g), q, g, lane, strict_upper);
+    put_half(sh.mb, 0, gram_rows<NV, 3>(sh.dy, sh.u, q, g), q, g, lane, strict_upper);
   } else if (wave == 1) {
     const float4v x = gram_rows<NV, NV>(sh.v, sh.dy, q, g);
     put_diag(sh.diag[1], x);
     put_half(sh.mr, 1, x, q, g, lane, strict);
     put_half(sh.mk, 0, gram_rows<NV, NV>(sh.dy, sh.v, q, g), q, g, lane, strict_upper);
-    put_half(sh.mv, 0, gram_rows<2, 2>(sh.r, sh.k, q, g), q, g, lane, upper);
+    put_half(sh.mv, 0, gram_rows<3, 3>(sh.r, sh.k, q, g), q, g, lane, upper);
   } else if (wave == 2) {
-    put_half(sh.ma, 0, gram_rows<2, 2>(sh.u, sh.z, q, g), q, g, lane, strict);
-    put_half(sh.mb, 1, gram_rows<2, 2>(sh.z, sh.u, q, g), q, g, lane, strict_upper);
+    put_half(sh.ma, 0, gram_rows<3, 3>(sh.u, sh.z, q, g), q, g, lane, strict);
+    put_half(sh.mb, 1, gram_rows<3, 3>(sh.z, sh.u, q, g), q, g, lane, strict_upper);
   } else {
-    put_half(sh.ma, 1, gram_rows<NV, 2>(sh.v, sh.z, q, g), q, g, lane, strict);
-    put_half(sh.mk, 1, gram_rows<2, NV>(sh.z, sh.v, q, g), q, g, lane, strict_upper);
-    put_half(sh.mv, 1, gram_rows<2, 2>(sh.a, sh.k, q, g), q, g, lane, strict_upper);
+    put_half(sh.ma, 1, gram_rows<NV, 3>(sh.v, sh.z, q, g), q, g, lane, strict);
+    put_half(sh.mk, 1, gram_rows<3, NV>(sh.z, sh.v, q, g), q, g, lane, strict_upper);
+    put_half(sh.mv, 1, gram_rows<3, 3>(sh.a, sh.k, q, g), q, g, lane, strict_upper);
   }
   __syncthreads();
 
@@ -300,32 +309,33 @@ __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Ch
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int row = row_block(q, 4 * h + g);
-    uint4 m[2], x[2];
-    auto rows = [&](const uint4(*from_)[128]) {
-      x[0] = from_[0][row];
-      x[1] = from_[1][row];
+    uint4 m[3], x[3];
+    auto rows = [&](const uint4(*from_)[128], int terms) {
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        if (n < terms) x[n] = from_[n][row];
     };
-    split8<2>(S + 8 * h, m);
-    rows(sh.dy);
-    dr = mul_terms<NV, 2>(x, m, dr);
-    rows(sh.z);
-    da = mul_terms<2, 2>(x, m, da);
-    split8<2>(D + 8 * h, m);
-    rows(sh.u);
-    db = mul_terms<2, 2>(x, m, db);
-    rows(sh.v);
-    dk = mul_terms<NV, 2>(x, m, dk);
-    split8<2>(Dv + 8 * h, m);
-    rows(sh.k);
-    dv = mul_terms<2, 2>(x, m, dv);
+    split8<3>(S + 8 * h, m);
+    rows(sh.dy, NV);
+    dr = mul_terms<NV, 3>(x, m, dr);
+    rows(sh.z, 3);
+    da = mul_terms<3, 3>(x, m, da);
+    split8<3>(D + 8 * h, m);
+    rows(sh.u, 3);
+    db = mul_terms<3, 3>(x, m, db);
+    rows(sh.v, NV);
+    dk = mul_terms<NV, 3>(x, m, dk);
+    split8<3>(Dv + 8 * h, m);
+    rows(sh.k, 3);
+    dv = mul_terms<3, 3>(x, m, dv);
   }
   const int ch = 16 * wave + 4 * (q & 3);
-  uint4 bk[2], ra[2], yz[2], m[2];
+  uint4 bk[3], ra[3], yz[3], m[3];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 3; ++i) {
     bk[i] = pair(rows4(sh.b[i], g, q, ch), rows4(sh.k[i], g, q, ch));
     ra[i] = pair(rows4(sh.r[i], g, q, ch), rows4(sh.a[i], g, q, ch));
-    yz[i] = pair(i < NV ? rows4(sh.dy[i], g, q, ch) : make_uint2(0, 0), rows4(sh.z[i], g, q, ch));
+    yz[i] = pair(i < NV ? rows4(sh.dy[i < NV ? i : 0], g, q, ch) : make_uint2(0, 0), rows4(sh.z[i], g, q, ch));
   }
   // sum_v D o S and the chunk's own part of it, before dB and dK get the rest
   float last = 0.f;
@@ -343,19 +353,19 @@ __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Ch
   last += __shfl_xor(last, 16);
   last += __shfl_xor(last, 32);
   auto mats = [&](const uint4(*x)[64]) {
-    m[0] = x[0][lane];
-    m[1] = x[1][lane];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) m[n] = x[n][lane];
   };
   mats(sh.mr);
-  dr = mul_terms<2, 2>(m, bk, dr);
+  dr = mul_terms<3, 3>(m, bk, dr);
   mats(sh.ma);
-  da = mul_terms<2, 2>(m, bk, da);
+  da = mul_terms<3, 3>(m, bk, da);
   mats(sh.mb);
-  db = mul_terms<2, 2>(m, ra, db);
+  db = mul_terms<3, 3>(m, ra, db);
   mats(sh.mk);
-  dk = mul_terms<2, 2>(m, ra, dk);
+  dk = mul_terms<3, 3>(m, ra, dk);
   mats(sh.mv);
-  dv = mul_terms<2, 2>(m, yz, dv);
+  dv = mul_terms<3, 3>(m, yz, dv);
 
   // decays: dL, then its sums from the end; lane (g, q) has tokens 4 g + i of
   // channel 16 w + q
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(256, 3) time_mix_grad_kernel(TimeMixBack b, Ch
   // through LDS to whole rows; the row operands are done with
   __syncthreads();
   uint16_t* out = (uint16_t*)&sh.a[0][0];  // [6][16][64]
-  static_assert(sizeof(sh.a) + sizeof(sh.r) + sizeof(sh.b) >= 6 * kChunk * kHead * 2, "outputs fit");
+  static_assert(sizeof(sh.a) + sizeof(sh.r) >= 6 * kChunk * kHead * 2, "outputs fit");
   const float4v all6[6] = {dr, dw, dk, dv, da, db};
 #pragma unroll
   for (int o = 0; o < 6; ++o)

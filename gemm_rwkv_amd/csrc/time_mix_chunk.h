@@ -45,18 +45,15 @@ __device__ __forceinline__ float cut(float x) {
   return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xffff0000u);
 }
 
-// Two fp32 values as NT bf16 pairs that add up to them: exactly for NT = 3
-// (8 bits each), within 2^-17 for NT = 2 (the last term is rounded).
+// Two fp32 values as NT bf16 pairs that add up to them, eight bits each:
+// NT = 3 holds fp32, NT = 2 the eleven bits of fp16, both exactly.
 template <int NT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t* t) {
   t[0] = high2(x, y);
   x -= cut(x);
   y -= cut(y);
-  if (NT == 2) {
-    t[1] = BF16::down2(x, y);
-    return;
-  }
   t[1] = high2(x, y);
+  if (NT == 2) return;
   x -= cut(x);
   y -= cut(y);
   t[2] = high2(x, y);

@@ -87,3 +87,85 @@ def test_outputs(lens, heads, kind, code):
     wy, ws = mix.time_mix(*(val[q] for q in "rwkvab"), lens, S)
     exactly(y, wy, "y")
     exactly(out, ws, "state")
+
+
+def backward_inputs(kind, tokens, nseq, heads, g):
+    """Rows with dy, states and their gradients; what is large comes in pairs
+    that differ by a small d and are read with opposite signs."""
+    x = {q: np.zeros((tokens, heads, 64)) for q in "rkvab"}
+    x["w"], x["dy"] = np.full((tokens, heads, 64), -6e4), np.zeros((tokens, heads, 64))
+    S, D = np.zeros((nseq, heads, 64, 64)), np.zeros((nseq, heads, 64, 64))
+    pair, odd = np.arange(tokens) // 2, np.arange(tokens) % 2
+    sign, even = (1 - 2 * odd)[:, None, None], (1 - odd)[:, None]
+    few = lambda *s: g.integers(0, 4, s)
+    rows = np.zeros((tokens, heads, 2))
+    rows[:, :, 0] = g.integers(128, 256, (tokens, heads))[2 * pair]
+    rows[:, :, 1] = g.integers(4, 256, (tokens, heads))[2 * pair] - odd[:, None] * few(tokens, heads)
+
+    def pairs(axis):               # [v][k] of 18 bits, paired along an axis
+        n = np.repeat(g.integers(1 << 17, 1 << 18, (nseq, heads, 64, 64)), 2, axis)
+        n = n.take(np.arange(64), axis)
+        low = few(nseq, heads, 64, 64) * (np.arange(64) % 2).reshape((64, 1) if axis == 2 else (1, 64))
+        return n - low
+
+    def signs(rows_):              # s, -s, s, -s ...
+        s = np.repeat(1 - 2 * g.integers(0, 2, (rows_, heads, 32)), 2, -1)
+        return s * (1 - 2 * (np.arange(64) % 2))
+
+    if kind == "dr of states":
+        S, x["dy"] = pairs(2), signs(tokens)
+    elif kind == "dv of states":
+        D, x["k"] = pairs(3), signs(tokens)
+    elif kind == "dk of states":
+        D, x["v"] = pairs(2), signs(tokens)
+    elif kind == "db of states":
+        D, S[..., 5] = pairs(2), signs(nseq)
+        x["a"][..., 5] = 1
+    elif kind == "da of states":
+        S, D[..., 7] = pairs(2), signs(nseq)
+        x["b"][..., 7] = 1
+    elif kind == "dr of removed":
+        S[..., 5], x["dy"] = pairs(2)[..., 5], signs(tokens)
+        x["a"][..., 5] = 1
+        x["b"][..., :1] = sign
+    elif kind == "dk of products":
+        x["v"][..., 0], x["v"][..., 1] = 1000 * even, even
+        x["dy"][..., :2] = rows
+        x["r"][:] = sign * g.integers(1, 4, (heads, 64))
+    elif kind == "dv of products":
+        x["k"][..., 0], x["k"][..., 1] = 1000 * even, even
+        x["r"][..., :2] = rows
+        x["dy"][:] = sign * g.integers(1, 4, (heads, 64))
+    else:                          # "dk of removed"
+        D[..., 7], x["v"] = pairs(2)[..., 7], signs(tokens)
+        x["b"][..., 7] = 1
+        x["a"][..., :1] = sign
+    return {q: z.reshape(tokens, -1) for q, z in x.items()}, S, D
+
+
+KINDS = ["dr of states", "dv of states", "dk of states", "db of states", "da of states", "dr of removed", "dk of products",
+         "dv of products", "dk of removed"]
+
+
+@pytest.mark.parametrize("code", TYPES, ids=IDS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,heads", [([2], 2), ([16], 2), ([70], 3), ([34, 2, 0, 40], 2)], ids=str)
+def test_gradients(lens, heads, kind, code):
+    say("exact", kind, lens, heads, code)
+    t, n, c = sum(lens), len(lens), 64 * heads
+    g = np.random.default_rng(t)
+    rows, S, D = backward_inputs(kind, t, n, heads, g)
+    dev, val = {}, {}
+    for q, z in rows.items():
+        dev[q], val[q] = device_rows(z, code)
+        assert q == "w" or np.array_equal(z, val[q])
+    outs = [torch.empty(t, c, dtype=TORCH[code], device="cuda") for _ in range(6)]
+    sd, dd = (torch.from_numpy(z).float().cuda() for z in (S, D))
+    din = torch.empty_like(sd)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    rq.rq_time_mix_backward(code, *(dev[q] for q in "rwkvab"), t, heads, c, cu, n, sd, dev["dy"], dd, *outs, din)
+    torch.cuda.synchronize()
+    want = mix.time_mix_backward(*(val[q] for q in "rwkvab"), lens, S, val["dy"], D)
+    for o, q in zip(outs, ("dr", "dw", "dk", "dv", "da", "db")):
+        exactly(o, want[q], q)
+    exactly(din, want["dstate"], "dstate")
