@@ -115,7 +115,7 @@ constexpr int kPad = 68;  // floats of a row of decays: 16-byte writes of 16 row
 template <int NV>
 struct GradLds {
   uint4 a[3][128], r[3][128], b[3][128], k[3][128], u[3][128], z[3][128], dy[NV][128], v[NV][128];
-  float fall[kChunk][kPad], sig[kChunk][kPad];
+  float fall[kChunk][kPad], slope[kChunk][kPad];  // decays from the chunk's start; the sigmoid's slope
   float diag[2][kChunk];  // of dQb and dQk, which are without it below
   uint4 mr[3][64];  // (dQb, dQk)
   uint4 ma[3][64];  // (dAb, dAk)
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(256, 2) time_mix_grad_kernel(TimeMixBack b, Ch
     }
     const size_t er = at * (kChunk * kHead) + q * kHead + 16 * wave + 4 * g;
     const float4v u = *(const float4v*)(from.U + er), z = *(const float4v*)(from.Z + er);
-    float x[4], fall[4], before[4], sig[4], grow[4];
+    float x[4], fall[4], before[4], slope[4], grow[4];
     auto up4 = [&](int i) {
       up2<T>(raw[i].x, x);
       up2<T>(raw[i].y, x + 2);
@@ -229,8 +229,9 @@ __global__ void __launch_bounds__(256, 2) time_mix_grad_kernel(TimeMixBack b, Ch
     up4(1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sig[i] = sigmoid_f32(x[i]);
-      float l = -(kDecay * kLog2e) * sig[i];
+      const float sig = sigmoid_f32(x[i]);
+      slope[i] = sig * sigmoid_f32(-x[i]);  // not sig (1 - sig), which cancels as sig nears 1
+      float l = -(kDecay * kLog2e) * sig;
       l += dpp<0x111>(l);
       l += dpp<0x112>(l);
       l += dpp<0x114>(l);
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(256, 2) time_mix_grad_kernel(TimeMixBack b, Ch
       before[i] = dpp_or<0x111>(1.f, fall[i]);
     }
     *(float4v*)&sh.fall[q][16 * wave + 4 * g] = float4v{fall[0], fall[1], fall[2], fall[3]};
-    *(float4v*)&sh.sig[q][16 * wave + 4 * g] = float4v{sig[0], sig[1], sig[2], sig[3]};
+    *(float4v*)&sh.slope[q][16 * wave + 4 * g] = float4v{slope[0], slope[1], slope[2], slope[3]};
     const int block = row_block(q, 2 * wave + (g >> 1)), half = g & 1;
     auto put3 = [&](uint4(*m)[128], float4v f) {
       uint2 t[3];
@@ -393,12 +394,11 @@ __global__ void __launch_bounds__(256, 2) time_mix_grad_kernel(TimeMixBack b, Ch
   float4v dw;
   {
     const float* fall = &sh.fall[4 * g][16 * wave + q];
-    const float* sig = &sh.sig[4 * g][16 * wave + q];
+    const float* slope = &sh.slope[4 * g][16 * wave + q];
     float f = g ? fall[-kPad] : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float s = sig[i * kPad];
-      dw[i] = (dl[i] + after) * (-kDecay * s * (1.f - s));
+      dw[i] = (dl[i] + after) * (-kDecay * slope[i * kPad]);
       da[i] *= f;
       f = fall[i * kPad];
       dr[i] *= f;
