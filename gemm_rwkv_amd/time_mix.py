@@ -4,8 +4,10 @@
     python -m gemm_rwkv_amd.time_mix --width 768 --prompts 5,37,300 --tokens 32
 
 ``shift_norm``, ``time_mix`` and ``head_gate`` are the library's operators as
-differentiable torch functions over contiguous rows [tokens][width] of fp16 or
-bf16; parameters and states are fp32.  ``TimeMix`` is the layer: ``train``
+differentiable torch functions over rows [tokens][width] of fp16 or bf16;
+parameters and states are fp32, offsets int32.  Other types, shapes that do not
+fit and tensors elsewhere than on the current GPU are refused (TypeError,
+ValueError).  ``TimeMix`` is the layer: ``train``
 runs it on its dense weights under autograd, ``serve`` on group-wise int4
 R/K/V/O weights, continuing the sequences whose states lie in slots (prompts
 of any lengths and single tokens, in one batch or in turn).
@@ -34,10 +36,45 @@ NORM_EPS, HEAD_EPS = 1e-5, 64e-5
 _CODE = {torch.float16: rq.RQ_F16, torch.bfloat16: rq.RQ_BF16}
 
 
-def _code(t):
-    if t.dtype not in _CODE:
-        raise TypeError("rows are float16 or bfloat16, not %s" % t.dtype)
-    return _CODE[t.dtype]
+def _rows(**rows):
+    """Refuses rows that are not of one 16-bit type and one shape [tokens][width]."""
+    (name, x), *others = rows.items()
+    if x.dtype not in _CODE:
+        raise TypeError("%s is %s, not float16 or bfloat16" % (name, x.dtype))
+    if x.dim() != 2:
+        raise ValueError("%s has shape %s, not [tokens][width]" % (name, list(x.shape)))
+    for other, t in others:
+        if t is not None:
+            _same(other, t, x.dtype, x.shape)
+
+
+def _same(name, t, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, not %s" % (name, list(t.shape), list(shape)))
+
+
+def _heads(x):
+    if x.shape[1] % HEAD:
+        raise ValueError("a width of %d is not in heads of %d" % (x.shape[1], HEAD))
+    return x.shape[1] // HEAD
+
+
+def _sequences(cu):
+    """How many sequences the offsets cu are of."""
+    if cu.dtype != torch.int32:
+        raise TypeError("cu is %s, not torch.int32" % cu.dtype)
+    if cu.dim() != 1 or cu.numel() == 0:
+        raise ValueError("cu has shape %s, not [sequences + 1]" % list(cu.shape))
+    return cu.numel() - 1
+
+
+def _on_gpu(*ts):
+    """The library's calls go to the current device."""
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.device.index == torch.cuda.current_device()):
+            raise ValueError("a tensor on %s; all have to be on the current GPU" % t.device)
 
 
 def _dense(*ts):
@@ -47,12 +84,21 @@ def _dense(*ts):
 class _ShiftNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, delta, mu, gamma, beta, shift, cu):
-        x, delta, mu, gamma, beta, shift = _dense(x, delta, mu, gamma, beta, shift)
-        (t, c), n = x.shape, cu.numel() - 1
+        _rows(x=x, delta=delta)
+        (t, c), n = x.shape, _sequences(cu)
+        if mu.dim() != 2:
+            raise ValueError("mu has shape %s, not [mixtures][width]" % list(mu.shape))
+        _same("mu", mu, torch.float32, (mu.shape[0], c))
+        _same("gamma", gamma, torch.float32, (c,))
+        _same("beta", beta, torch.float32, (c,))
+        if shift is not None:
+            _same("shift", shift, x.dtype, (n, c))
+        _on_gpu(x, delta, mu, gamma, beta, shift, cu)
+        x, delta, mu, gamma, beta, shift, cu = _dense(x, delta, mu, gamma, beta, shift, cu)
         full = x if delta is None else torch.empty_like(x)
         out = torch.empty(mu.shape[0], t, c, dtype=x.dtype, device=x.device)
         last = torch.empty(n, c, dtype=x.dtype, device=x.device)
-        rq.rq_shift_norm(_code(x), x, delta, 1.0, t, c, c, cu, n, gamma, beta, NORM_EPS, mu, mu.shape[0], shift, last, None, n,
+        rq.rq_shift_norm(_CODE[x.dtype], x, delta, 1.0, t, c, c, cu, n, gamma, beta, NORM_EPS, mu, mu.shape[0], shift, last, None, n,
                          None if delta is None else full, out, c)
         ctx.save_for_backward(full, mu, gamma, beta, shift, cu)
         ctx.with_delta = delta is not None
@@ -69,7 +115,7 @@ class _ShiftNorm(torch.autograd.Function):
         dx = torch.empty_like(x)
         dshift = None if shift is None else torch.empty_like(shift)
         dgamma, dbeta, dmu = torch.empty_like(gamma), torch.empty_like(beta), torch.empty_like(mu)
-        rq.rq_shift_norm_backward(_code(x), x, 1.0, t, c, c, cu, n, gamma, beta, NORM_EPS, mu, mu.shape[0], shift, dout, c,
+        rq.rq_shift_norm_backward(_CODE[x.dtype], x, 1.0, t, c, c, cu, n, gamma, beta, NORM_EPS, mu, mu.shape[0], shift, dout, c,
                                   dfull, dlast, dx, None, dshift, dgamma, dbeta, dmu)
         return dx, dx if ctx.with_delta else None, dmu, dgamma, dbeta, dshift, None
 
@@ -77,12 +123,18 @@ class _ShiftNorm(torch.autograd.Function):
 class _TimeMix(torch.autograd.Function):
     @staticmethod
     def forward(ctx, r, w, k, v, a, b, state, cu):
+        _rows(r=r, w=w, k=k, v=v, a=a, b=b)
+        (t, c), n = r.shape, _sequences(cu)
+        if state is None:
+            _heads(r)
+        else:
+            _same("state", state, torch.float32, (n, _heads(r), HEAD, HEAD))
+        _on_gpu(r, w, k, v, a, b, state, cu)
         rows = _dense(r, w, k, v, a, b)
-        state, = _dense(state)
-        (t, c), n = r.shape, cu.numel() - 1
+        state, cu = _dense(state, cu)
         y = torch.empty_like(rows[0])
         last = torch.empty(n, c // HEAD, HEAD, HEAD, dtype=torch.float32, device=r.device)
-        rq.rq_time_mix(_code(r), *rows, t, c // HEAD, c, cu, n, state, last, None, n, y, c)
+        rq.rq_time_mix(_CODE[r.dtype], *rows, t, c // HEAD, c, cu, n, state, last, None, n, y, c)
         ctx.save_for_backward(*rows, state, cu)
         ctx.set_materialize_grads(False)
         return y, last
@@ -96,18 +148,23 @@ class _TimeMix(torch.autograd.Function):
             dy = torch.zeros_like(rows[0])
         grads = [torch.empty_like(x) for x in rows]
         dstate = None if state is None else torch.empty_like(state)
-        rq.rq_time_mix_backward(_code(dy), *rows, t, c // HEAD, c, cu, n, state, dy, dlast, *grads, dstate)
+        rq.rq_time_mix_backward(_CODE[dy.dtype], *rows, t, c // HEAD, c, cu, n, state, dy, dlast, *grads, dstate)
         return (*grads, dstate, None)
 
 
 class _HeadGate(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, r, k, v, g, gamma, beta, u):
+        _rows(y=y, r=r, k=k, v=v, g=g)
+        _heads(y)
+        for name, param in (("gamma", gamma), ("beta", beta), ("u", u)):
+            _same(name, param, torch.float32, y.shape[1:])
+        _on_gpu(y, r, k, v, g, gamma, beta, u)
         rows = _dense(y, r, k, v, g)
         params = _dense(gamma, beta, u)
         t, c = y.shape
         out = torch.empty_like(rows[0])
-        rq.rq_head_gate(_code(y), *rows, t, c // HEAD, c, params[0], params[1], HEAD_EPS, params[2], out, c)
+        rq.rq_head_gate(_CODE[y.dtype], *rows, t, c // HEAD, c, params[0], params[1], HEAD_EPS, params[2], out, c)
         ctx.save_for_backward(*rows, *params)
         return out
 
@@ -117,7 +174,7 @@ class _HeadGate(torch.autograd.Function):
         t, c = dout.shape
         grads = [torch.empty_like(x) for x in rows]
         dparams = [torch.empty_like(x) for x in (gamma, beta, u)]
-        rq.rq_head_gate_backward(_code(dout), *rows, t, c // HEAD, c, gamma, beta, HEAD_EPS, u, dout.contiguous(), *grads, *dparams)
+        rq.rq_head_gate_backward(_CODE[dout.dtype], *rows, t, c // HEAD, c, gamma, beta, HEAD_EPS, u, dout.contiguous(), *grads, *dparams)
         return (*grads, *dparams)
 
 
@@ -205,9 +262,18 @@ class TimeMix:
             raise RuntimeError("call quantize() first")
         if self.dtype != torch.float16:
             raise TypeError("the quantized products take float16")
-        p, (m, c), n = self.params, x.shape, cu.numel() - 1
-        heads, nslots = c // HEAD, shift.shape[0]
-        x, delta = _dense(x, delta)
+        _rows(x=x, delta=delta)
+        p, n, heads, nslots = self.params, _sequences(cu), self.width // HEAD, shift.shape[0]
+        _same("x", x, self.dtype, (x.shape[0], self.width))
+        _same("shift", shift, self.dtype, (nslots, self.width))
+        _same("state", state, torch.float32, (nslots, heads, HEAD, HEAD))
+        if not (shift.is_contiguous() and state.is_contiguous()):
+            raise ValueError("shift and state are updated in place and have to be contiguous")
+        if slots is not None:
+            _same("slots", slots, torch.int32, (n,))
+        _on_gpu(x, delta, cu, shift, state, slots)
+        m, c = x.shape
+        x, delta, cu, slots = _dense(x, delta, cu, slots)
         full = x if delta is None else torch.empty_like(x)
         mixes = torch.empty(len(MIXTURES), m, c, dtype=x.dtype, device=x.device)
         rq.rq_shift_norm(rq.RQ_F16, x, delta, 1.0, m, c, c, cu, n, p["gamma"], p["beta"], NORM_EPS, p["mu"], len(MIXTURES),
