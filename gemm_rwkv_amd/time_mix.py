@@ -7,7 +7,8 @@
 differentiable torch functions over rows [tokens][width] of fp16 or bf16;
 parameters and states are fp32, offsets int32.  Other types, shapes that do not
 fit and tensors elsewhere than on the current GPU are refused (TypeError,
-ValueError).  ``TimeMix`` is the layer: ``train``
+ValueError).  They are differentiable once: a gradient of their gradient is an
+error.  ``TimeMix`` is the layer: ``train``
 runs it on its dense weights under autograd, ``serve`` on group-wise int4
 R/K/V/O weights, continuing the sequences whose states lie in slots (prompts
 of any lengths and single tokens, in one batch or in turn).
@@ -27,6 +28,7 @@ import sys
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 from . import rq
 
@@ -106,6 +108,7 @@ class _ShiftNorm(torch.autograd.Function):
         return (full if ctx.with_delta else x.view_as(x)), out, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dfull, dout, dlast):
         x, mu, gamma, beta, shift, cu = ctx.saved_tensors
         (t, c), n = x.shape, cu.numel() - 1
@@ -140,6 +143,7 @@ class _TimeMix(torch.autograd.Function):
         return y, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dlast):
         *rows, state, cu = ctx.saved_tensors
         (t, c), n = rows[0].shape, cu.numel() - 1
@@ -169,6 +173,7 @@ class _HeadGate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         *rows, gamma, beta, u = ctx.saved_tensors
         t, c = dout.shape
