@@ -83,6 +83,13 @@ def _dense(*ts):
     return [t if t is None else t.contiguous() for t in ts]
 
 
+def _workspace(x):
+    """Memory for one call: of torch's allocator on the current stream, so that
+    calls on other streams and threads, whose kernels may run at the same time,
+    have other memory.  (These entries leave its split counters alone.)"""
+    return torch.empty(rq.rq_workspace_bytes(), dtype=torch.uint8, device=x.device)
+
+
 class _ShiftNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, delta, mu, gamma, beta, shift, cu):
@@ -119,7 +126,7 @@ class _ShiftNorm(torch.autograd.Function):
         dshift = None if shift is None else torch.empty_like(shift)
         dgamma, dbeta, dmu = torch.empty_like(gamma), torch.empty_like(beta), torch.empty_like(mu)
         rq.rq_shift_norm_backward(_CODE[x.dtype], x, 1.0, t, c, c, cu, n, gamma, beta, NORM_EPS, mu, mu.shape[0], shift, dout, c,
-                                  dfull, dlast, dx, None, dshift, dgamma, dbeta, dmu)
+                                  dfull, dlast, dx, None, dshift, dgamma, dbeta, dmu, ws=_workspace(x))
         return dx, dx if ctx.with_delta else None, dmu, dgamma, dbeta, dshift, None
 
 
@@ -137,7 +144,7 @@ class _TimeMix(torch.autograd.Function):
         state, cu = _dense(state, cu)
         y = torch.empty_like(rows[0])
         last = torch.empty(n, c // HEAD, HEAD, HEAD, dtype=torch.float32, device=r.device)
-        rq.rq_time_mix(_CODE[r.dtype], *rows, t, c // HEAD, c, cu, n, state, last, None, n, y, c)
+        rq.rq_time_mix(_CODE[r.dtype], *rows, t, c // HEAD, c, cu, n, state, last, None, n, y, c, ws=_workspace(y))
         ctx.save_for_backward(*rows, state, cu)
         ctx.set_materialize_grads(False)
         return y, last
@@ -179,7 +186,8 @@ class _HeadGate(torch.autograd.Function):
         t, c = dout.shape
         grads = [torch.empty_like(x) for x in rows]
         dparams = [torch.empty_like(x) for x in (gamma, beta, u)]
-        rq.rq_head_gate_backward(_CODE[dout.dtype], *rows, t, c // HEAD, c, gamma, beta, HEAD_EPS, u, dout.contiguous(), *grads, *dparams)
+        rq.rq_head_gate_backward(_CODE[dout.dtype], *rows, t, c // HEAD, c, gamma, beta, HEAD_EPS, u, dout.contiguous(), *grads, *dparams,
+                                 ws=_workspace(dout))
         return (*grads, *dparams)
 
 
@@ -254,15 +262,18 @@ class TimeMix:
         y, after = time_mix(r, w, k, v, a, b, cu, state)
         return full, F.linear(head_gate(y, r, k, v, g, p["head_gamma"], p["head_beta"], p["u"]), p["W_o"]), last, after
 
-    def _product(self, x, q):
+    def _product(self, x, q, ws):
         m, c = x.shape
         y = torch.empty_like(x)
-        return (rq.rq_gemm_small_m if m <= 32 else rq.rq_gemm_w4)(x, m, c, self.quantized[q], y, c)
+        return (rq.rq_gemm_small_m if m <= 32 else rq.rq_gemm_w4)(x, m, c, self.quantized[q], y, c, ws=ws)
 
     @torch.no_grad()
-    def serve(self, x, delta, cu, shift, state, slots):
+    def serve(self, x, delta, cu, shift, state, slots, ws=None):
         """(x + delta, the layer's output) of sequences that continue the
-        entries slots[i] of shift and state, which are updated in place."""
+        entries slots[i] of shift and state, which are updated in place.  ws:
+        a workspace of rq.rq_workspace_bytes() bytes, zeroed once; calls that
+        may run at the same time, on several streams, need one each (None: the
+        binding's, which all calls without one share)."""
         if self.quantized is None:
             raise RuntimeError("call quantize() first")
         if self.dtype != torch.float16:
@@ -285,15 +296,15 @@ class TimeMix:
                          shift, shift, slots, nslots, None if delta is None else full, mixes, c)
         if m <= 32:
             r, k, v = (torch.empty_like(x) for _ in range(3))
-            rq.rq_fused_rkv(mixes[0], mixes[2], mixes[3], m, c, *(self.quantized[q] for q in "rkv"), r, k, v, c)
+            rq.rq_fused_rkv(mixes[0], mixes[2], mixes[3], m, c, *(self.quantized[q] for q in "rkv"), r, k, v, c, ws=ws)
         else:
-            r, k, v = (self._product(mixes[i], q) for i, q in ((0, "r"), (2, "k"), (3, "v")))
+            r, k, v = (self._product(mixes[i], q, ws) for i, q in ((0, "r"), (2, "k"), (3, "v")))
         w, g, k, a, b = self._inner(mixes, k)
         y = torch.empty_like(x)
-        rq.rq_time_mix(rq.RQ_F16, r, w, k, v, a, b, m, heads, c, cu, n, state, state, slots, nslots, y, c)
+        rq.rq_time_mix(rq.RQ_F16, r, w, k, v, a, b, m, heads, c, cu, n, state, state, slots, nslots, y, c, ws=ws)
         gated = torch.empty_like(x)
         rq.rq_head_gate(rq.RQ_F16, y, r, k, v, g, m, heads, c, p["head_gamma"], p["head_beta"], HEAD_EPS, p["u"], gated, c)
-        return full, self._product(gated, "o")
+        return full, self._product(gated, "o", ws)
 
 
 def offsets(lens, device="cuda"):
