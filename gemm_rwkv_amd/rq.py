@@ -402,14 +402,17 @@ def rq_gemm_int8_acc(xq, m, w, acc, stream=None, ws=None):
 
 def _fresh_ws(ws, nbytes, stream):
     """(pointer, bytes, tensor) of a workspace that must hold nbytes: the
-    caller's, or, for None, memory of torch's allocator for this call."""
+    caller's, or, for None, memory of torch's allocator for this call.  It is
+    taken from the pool of the stream that the call goes to: a block of the
+    current stream's pool may still be in use there."""
     if ws is not None or not _gpu():
         return _ws(False if ws is None else ws) + (None,)
-    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        t.record_stream(stream)
+    if stream is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    else:
+        handle = _stream(stream)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
+            t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     return t.data_ptr(), nbytes, t
 
 

@@ -32,3 +32,32 @@ def test_gradient_of_flat_decays(raw, code):
     want = mix.time_mix_backward(*(val[q] for q in "rwkvab"), lens, state, dy)
     for o, q in zip(outs, ("dr", "dw", "dk", "dv", "da", "db")):
         close(o.get(), want[q], code, q)
+
+
+def test_gradient_on_given_streams():
+    """The launch stream as an argument, as an object, a handle and the null
+    stream, between calls on the current one: the same bits."""
+    code, heads, lens = rq.RQ_F16, 2, [300, 41]
+    t, c, n = sum(lens), 128, 2
+    say("gradient on given streams")
+    dev, _, g = mix_inputs(lens, heads, code, c, 72)
+    dy, cu = rows(g.standard_normal((t, c)), code, c)[0], offsets(lens)
+
+    def go(**kw):
+        outs = [torch.empty(t, c, dtype=torch.float16, device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            rq.rq_time_mix_backward(code, *(dev[q] for q in "rwkvab"), t, heads, c, cu, n, None, dy, None, *outs, None, **kw)
+        return outs
+
+    want, side = go(), torch.cuda.Stream()
+    for kw in ({"stream": side}, {}, {"stream": side.cuda_stream}, {"stream": 0}):
+        got = go(**kw)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), kw
+    with torch.cuda.stream(side):
+        got = go(stream=0)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
