@@ -23,8 +23,8 @@ __global__ void __launch_bounds__(256) head_gate_kernel(HeadGate p, int rows) {
   load8f(p.gamma + c, gamma);
   load8f(p.beta + c, beta);
   load8f(p.u + c, u);
-  const int t1 = min(p.tokens, (int)(blockIdx.x + 1) * rows);
-  for (int t = blockIdx.x * rows; t < t1; ++t) {
+  const int t0 = blockIdx.x * rows, t1 = run_end(p.tokens, t0, rows);
+  for (int t = t0; t < t1; ++t) {
     const size_t at = (size_t)t * p.ld + c;
     float y[8], r[8], k[8], v[8], g[8];
     load8<T>(p.y, at, y);
@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(256) head_gate_kernel(HeadGate p, int rows) {
 hipError_t launch_head_gate(const HeadGate& p, bool bf16, hipStream_t st) {
   const int width = p.heads * kHead;
   const int cols = (width / 8 + 255) / 256;
-  const int rows = 1 + p.tokens / (1 << 20);  // a grid of at most 2^20 rows
-  const dim3 grid((p.tokens + rows - 1) / rows, cols);
+  const int rows = gate_rows(p.tokens);
+  const dim3 grid(run_count(p.tokens, rows), cols);
   if (bf16)
     hipLaunchKernelGGL(head_gate_kernel<BF16>, grid, dim3(256), 0, st, p, rows);
   else
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(256) head_gate_back_kernel(HeadGateBack b, int
     load8f(p.gamma + c, gamma);
     load8f(p.beta + c, beta);
     load8f(p.u + c, u);
-    const int t1 = min(p.tokens, (int)(blockIdx.x + 1) * rows);
-    for (int t = blockIdx.x * rows + wave; t < t1; t += 4) {
+    const int t0 = blockIdx.x * rows, t1 = run_end(p.tokens, t0, rows);
+    for (int t = t0 + wave; t < t1; t += 4) {
       const size_t at = (size_t)t * p.ld + c;
       float y[8], r[8], k[8], v[8], g[8], d[8];
       load8<T>(p.y, at, y);
@@ -219,14 +219,14 @@ hipError_t launch_head_gate_back(const HeadGateBack& b, bool bf16, hipStream_t s
   const int cols = (width + 511) / 512;
   // rows per workgroup: about 1024 workgroups, at least 16 rows each, and no
   // more partial sums than the workspace holds
-  int64_t groups = (p.tokens + 15) / 16;
+  int64_t groups = run_count(p.tokens, 16);
   const int64_t want = (1024 + cols - 1) / cols;
   if (groups > want) groups = want;
   const int64_t fit = b.parts ? (int64_t)(b.parts_bytes / ((size_t)width * 12)) : 0;
   if (groups > fit) groups = fit;
   if (groups < 1) groups = 1;
-  const int rows = (int)((p.tokens + groups - 1) / groups);
-  if (rows > 0) groups = (p.tokens + rows - 1) / rows;
+  const int rows = run_rows(p.tokens, (int)groups);
+  if (p.tokens > 0) groups = run_count(p.tokens, rows);
   const dim3 grid((unsigned)groups, cols);
   if (bf16)
     hipLaunchKernelGGL(head_gate_back_kernel<BF16>, grid, dim3(256), 0, st, b, rows);

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "device_common.h"
+#include "runs.h"
 
 namespace rq {
 

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(512) shift_norm_kernel(ShiftNorm p, int rows, 
   };
   const float inv = 1.f / (float)width;
 
-  const int t0 = blockIdx.x * rows, t1 = min(p.seq.tokens, t0 + rows);
+  const int t0 = blockIdx.x * rows, t1 = run_end(p.seq.tokens, t0, rows);
   int s = seq_of(p.seq, t0), begin, end;
   seq_span(p.seq, s, begin, end);
   // Each turn has row t in h, its mean, and row t + 1 on its way; one barrier
@@ -266,14 +266,8 @@ int threads_of(int width, int nv) { return (width / 8 + nv * 64 - 1) / (nv * 64)
 
 hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
   const int nv = p.width > 4096 ? 2 : 1;
-  // A run's first row costs the norm of the row before it, a long one leaves
-  // compute units idle.  Rows one, two, four, eight at a time, in us, at width
-  // 2048 with six mixtures and at width 2560 with one: 600 rows 9.7 10.8 14 22
-  // and 7.7 7.6 9.1 13; 1025 rows 12.8 12.9 16 24 and 11 8.7 10 14; 2048 rows 22
-  // 18 19 27 and 20 16 14 16; 4099 rows 42 35 35 38 and 34 27 25 23; 16384 rows
-  // 139 134 132 153 and 117 86 77 78.
-  const int rows = p.seq.tokens <= 768 ? 1 : p.seq.tokens <= 1536 ? 2 : 4 + p.seq.tokens / (1 << 22);
-  const int tiles = (p.seq.tokens + rows - 1) / rows;
+  const int rows = norm_rows(p.seq.tokens);
+  const int tiles = run_count(p.seq.tokens, rows);
   const int empty = p.shift_out && (p.seq.cu || p.seq.tokens == 0) && p.shift_out != p.shift_in ? p.seq.nseq : 0;
   if (tiles + empty == 0) return hipSuccess;
   const dim3 grid(tiles + empty), block(threads_of(p.width, nv));
@@ -336,7 +330,7 @@ __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[j][i] = (x[j][i] - mean) * rstd;
   };
-  const int t0 = blockIdx.x * rows, t1 = min(p.seq.tokens, t0 + rows);
+  const int t0 = blockIdx.x * rows, t1 = run_end(p.seq.tokens, t0, rows);
   if (t0 < t1) {
     int s = seq_of(p.seq, t0), begin, end;
     seq_span(p.seq, s, begin, end);
@@ -560,8 +554,8 @@ hipError_t launch_shift_norm_back(const ShiftNormBack& p, bool bf16, hipStream_t
   if (groups > fit) groups = fit;
   if (groups > p.seq.tokens) groups = p.seq.tokens;
   if (groups < 1) groups = 1;
-  const int rows = (int)((p.seq.tokens + groups - 1) / groups);
-  if (rows > 0) groups = (p.seq.tokens + rows - 1) / rows;
+  const int rows = run_rows(p.seq.tokens, (int)groups);
+  if (p.seq.tokens > 0) groups = run_count(p.seq.tokens, rows);
   const dim3 grid((unsigned)groups), block((p.width / 4 + nv * 64 - 1) / (nv * 64) * 64);
   const hipError_t e = bf16 ? (nv == 1 ? start_back<BF16, 1>(p, rows, grid, block, st) : start_back<BF16, 2>(p, rows, grid, block, st))
                             : (nv == 1 ? start_back<F16, 1>(p, rows, grid, block, st) : start_back<F16, 2>(p, rows, grid, block, st));
