@@ -71,7 +71,7 @@ hipError_t launch_head_gate(const HeadGate& p, bool bf16, hipStream_t st) {
 // is fixed.  Bound by memory: 4096 tokens of width 2048 in bf16 take 39 to 44
 // us, 4.2 to 4.7 TB/s, and the sums of the partial rows 5 us more.
 template <typename T>
-__global__ void __launch_bounds__(256) head_gate_back_kernel(HeadGateBack b, int rows) {
+__global__ void __launch_bounds__(256, 4) head_gate_back_kernel(HeadGateBack b, int rows) {
   const HeadGate& p = b.f;
   __shared__ float red[4][24][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(256) head_gate_back_kernel(HeadGateBack b, int
     load8f(p.gamma + c, gamma);
     load8f(p.beta + c, beta);
     load8f(p.u + c, u);
-    const int t0 = blockIdx.x * rows, t1 = run_end(p.tokens, t0, rows);
-    for (int t = t0 + wave; t < t1; t += 4) {
+    const int t1 = run_end(p.tokens, blockIdx.x * rows, rows);
+    for (int t = blockIdx.x * rows + wave; t < t1; t += 4) {
       const size_t at = (size_t)t * p.ld + c;
       float y[8], r[8], k[8], v[8], g[8], d[8];
       load8<T>(p.y, at, y);
