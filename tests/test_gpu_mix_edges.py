@@ -61,3 +61,46 @@ def test_gradient_on_given_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# two and four rows per workgroup, with one and two vectors of a row per thread
+@pytest.mark.parametrize("code", TYPES, ids=IDS)
+@pytest.mark.parametrize("lens", [[700, 0, 600], [1300], [900, 0, 801]], ids=str)
+@pytest.mark.parametrize("width,nmix", [(2568, 3), (4104, 2), (8192, 1)])
+def test_many_wide_rows(lens, width, nmix, code):
+    t, n, ld = sum(lens), len(lens), width + 8
+    say("many wide rows", lens, width, nmix, code)
+    g = np.random.default_rng(t + width + 2)
+    x, delta = (rows(3 * g.standard_normal((t, width)) + 1, code, ld) for _ in range(2))
+    shift, dsh = (rows(g.standard_normal((n, width)), code, width) for _ in range(2))
+    pd = [torch.from_numpy(z.astype(np.float32)).cuda() for z in (g.standard_normal(width), g.standard_normal(width),
+                                                                  g.random((nmix, width)))]
+    par = [z.double().cpu().numpy() for z in pd]
+    xo, out = Out(t, width, ld, code), Out(nmix * t, width, ld, code)
+    new = torch.full((n, width), float("nan"), dtype=shift[0].dtype, device="cuda")
+    rq.rq_shift_norm(code, x[0], delta[0], -0.75, t, width, ld, offsets(lens), n, pd[0], pd[1], 1e-5, pd[2], nmix, shift[0],
+                     new, None, n, xo.ptr(), out.ptr(), ld)
+    torch.cuda.synchronize()
+    wx, wo, last = mix.shift_norm(x[1], delta[1], -0.75, lens, par[0], par[1], 1e-5, par[2], shift[1])
+    close(xo.get(), wx, code, "x")
+    close(out.get(), wo.reshape(nmix * t, width), code, "out")
+    close(new, last, code, "shift")
+    # in place: the row left behind replaces the one that the first row read
+    out2, same = Out(nmix * t, width, ld, code), shift[0].clone()
+    rq.rq_shift_norm(code, x[0], delta[0], -0.75, t, width, ld, offsets(lens), n, pd[0], pd[1], 1e-5, pd[2], nmix, same, same,
+                     None, n, None, out2.ptr(), ld)
+    torch.cuda.synchronize()
+    assert torch.equal(out2.get(), out.get()) and torch.equal(same, new)
+    # the gradient
+    up, dout = rows(g.standard_normal((t, width)), code, ld), rows(g.standard_normal((nmix * t, width)), code, ld)
+    dx, din = Out(t, width, ld, code), Out(n, width, width, code)
+    f32 = dict(dtype=torch.float32, device="cuda")
+    dg, db, dm = (torch.full(s, float("nan"), **f32) for s in ((width,), (width,), (nmix, width)))
+    rq.rq_shift_norm_backward(code, x[0], 0.5, t, width, ld, offsets(lens), n, pd[0], pd[1], 1e-5, pd[2], nmix, shift[0],
+                              dout[0], ld, up[0], dsh[0], dx.ptr(), None, din.ptr(), dg, db, dm)
+    torch.cuda.synchronize()
+    want = mix.shift_norm_backward(x[1], lens, par[0], par[1], 1e-5, par[2], shift[1], dout[1].reshape(nmix, t, width), up[1], dsh[1])
+    close(dx.get(), want["dx"], code, "dx")
+    close(din.get(), want["dshift_in"], code, "dshift_in")
+    for z, q in ((dg, "dgamma"), (db, "dbeta"), (dm, "dmu")):
+        close(z, want[q], code, q)
