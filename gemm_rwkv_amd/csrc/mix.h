@@ -137,6 +137,8 @@ size_t time_mix_back_bytes(int64_t tokens, int64_t heads, int64_t nseq);
 // 16-bit element types: widening is exact, narrowing rounds to nearest even
 struct F16 {
   static constexpr uint32_t kMinusInf2 = 0xfc00fc00u;
+  // nonzero if one of two values is an infinity or NaN: its exponent's carry
+  static __device__ __forceinline__ uint32_t not_finite2(uint32_t v) { return ((v & 0x7fff7fffu) + 0x04000400u) & 0x80008000u; }
   static __device__ __forceinline__ float up(uint32_t lo16) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)lo16);
   }
@@ -147,6 +149,7 @@ struct F16 {
 };
 struct BF16 {
   static constexpr uint32_t kMinusInf2 = 0xff80ff80u;
+  static __device__ __forceinline__ uint32_t not_finite2(uint32_t v) { return ((v & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
   static __device__ __forceinline__ float up(uint32_t lo16) { return __builtin_bit_cast(float, lo16 << 16); }
   static __device__ __forceinline__ uint32_t down2(float a, float b) {
     typedef __bf16 bf2 __attribute__((ext_vector_type(2)));

@@ -168,6 +168,9 @@ __device__ __forceinline__ void walk_out(const TimeMix& p, const Segment& sg, Ch
         if (4 * g + i < left) to[(size_t)i * p.ldy] = (uint16_t)((i < 2 ? y01 : y23) >> (16 * (i & 1)));
     }
     to += (size_t)kChunk * p.ldy;
+  }, [&](int c) {
+    const int t = sg.begin + c * kChunk;
+    return step_tokens<T>(p, head, t, min(kChunk, sg.end - t), st, wave, lane);
   });
 }
 
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_segment_kernel(TimeM
     st.load(nullptr, part, lane);
   auto none = [](int, float4v) {};
   const int chunks = (sg.end - sg.begin) / kChunk;  // whole: only a last segment is ragged
-  walk_chunks<T, false, false>(st, chunks, sh, part, lane, map ? 0u : ~0u, [](int) {}, none, none);
+  walk_chunks<T, false, false>(st, chunks, sh, part, lane, map ? 0u : ~0u, [](int) {}, none, none, [](int) { return float4v{}; });
   st.store(to + (map ? kHead * kHead : 0), part, lane);
 }
 

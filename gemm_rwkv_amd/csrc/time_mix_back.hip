@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chains_kernel(TimeMi
   const size_t state = ((size_t)s * p.heads + head) * kState;
   const size_t at = ((size_t)first_chunk(begin, s) * p.heads + head);
   auto out = [](int, float4v) {};
+  auto steps = [](int) { return float4v{}; };
   auto rows = [&](float* base, int c, float4v u) {
     float* to = base + (at + (size_t)c * p.heads) * (kChunk * kHead) + 4 * g * kHead + 16 * wave + q;
 #pragma unroll
@@ -95,13 +96,13 @@ __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chains_kernel(TimeMi
     st.load(p.state_in ? p.state_in + state : nullptr, wave, lane);
     walk_chunks<T, false, false>(
         st, chunks, sh, wave, lane, ~0u, [&](int c) { st.store(to.S + (at + (size_t)c * p.heads) * kState, wave, lane); },
-        [&](int c, float4v u) { rows(to.U, c, u); }, out);
+        [&](int c, float4v u) { rows(to.U, c, u); }, out, steps);
   } else {
     st.load(b.dstate_out ? b.dstate_out + state : nullptr, wave, lane);
     walk_chunks<T, false, true>(
         st, chunks, sh, wave, lane, ~0u,
         [&](int c) { st.store(to.D + (at + (size_t)(chunks - 1 - c) * p.heads) * kState, wave, lane); },
-        [&](int c, float4v u) { rows(to.Z, chunks - 1 - c, u); }, out);
+        [&](int c, float4v u) { rows(to.Z, chunks - 1 - c, u); }, out, steps);
     if (b.dstate_in) st.store(b.dstate_in + state, wave, lane);
   }
 }

@@ -119,7 +119,9 @@ struct ChunkOps {
   uint4 k[3][16 * 8];
   uint4 v[2][16 * 8];   // V rows, two bf16 terms (one for bf16 rows)
   float end[64];        // exp L_15 by channel
+  int odd;              // what is not finite: kOddRows, kOddValues
 };
+constexpr int kOddRows = 1, kOddValues = 2;
 
 // Block c (eight channels) of row t.  A transposing read takes four rows and
 // two of every four channels of half a row at once; turning the halves of
@@ -361,6 +363,17 @@ struct ChunkPrep {
 #pragma unroll
     for (int n = 0; n < 3; ++n) o.ak[n][lane] = t[n];
     if (!OUT) return;
+    // every row of A, B and K is in ab and ak
+    float zero = 0.f;
+    uint32_t values = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zero += ab[i] + ak[i];
+    zero *= 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      values |= T::not_finite2(raw[3][h].x) | T::not_finite2(raw[3][h].y) | T::not_finite2(raw[3][h].z) | T::not_finite2(raw[3][h].w);
+    const int odd = (__builtin_amdgcn_ballot_w64(zero != zero) ? kOddRows : 0) | (__builtin_amdgcn_ballot_w64(values != 0) ? kOddValues : 0);
+    if (lane == 0) o.odd = odd;
     float4v qbm = qb, qkm = qk;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -428,10 +441,12 @@ struct ChunkHead {
   uint4 a[2][3];
   uint2 ak[3], v[kV], t[3];
   float4v end[4];
+  int odd;
 
   // values: all ones, or 0 to take V for zeros (the map alone)
   __device__ __forceinline__ void fetch(const ChunkOps& o, int wave, int lane, uint32_t values) {
     const int q = lane & 15, g = lane >> 4;
+    odd = o.odd;  // first, because it is looked at first
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -473,6 +488,79 @@ __device__ __forceinline__ void interleave() {
     if (READS) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
     if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
   }
+}
+
+// The columns (channels of v, of this wave's sixteen) in which a lane has `on`.
+__device__ __forceinline__ uint32_t columns(bool on) {
+  uint64_t m = __builtin_amdgcn_ballot_w64(on);
+  m |= m >> 32;
+  return (uint32_t)(m | m >> 16) & 0xffffu;
+}
+
+// Whether what is not finite in a chunk would reach the outputs of tokens before
+// it: the triangular products multiply what a later token has with zeros, which
+// makes NaN of it.  In a column whose state is not finite already none of the
+// outputs is, in whatever way they are summed.  (R reaches its own row only.)
+template <typename T, bool REV>
+__device__ __forceinline__ bool leaks(const ChunkState& st, const ChunkHead<T, REV>& hd, int odd) {
+  uint32_t hurt = 0, held = 0;
+#pragma unroll
+  for (int n = 0; n < ChunkHead<T, REV>::kV; ++n) hurt |= BF16::not_finite2(hd.v[n].x) | BF16::not_finite2(hd.v[n].y);
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = st.X[n][i];
+      held |= (__builtin_bit_cast(uint32_t, s) & 0x7f800000u) == 0x7f800000u;
+    }
+  return (((odd & kOddRows) ? 0xffffu : columns(hurt != 0)) & ~columns(held != 0)) != 0;
+}
+
+// A chunk's n tokens one after the other, for one that leaks: Y as chunk_step
+// lays it out.  Rows come straight from memory.
+template <typename T>
+__device__ __forceinline__ float4v step_tokens(const TimeMix& p, int head, int t0, int n, ChunkState& st, int wave, int lane) {
+  asm volatile("" : "+v"(lane));  // nothing of this is kept in registers over the chunks
+  const int q = lane & 15, g = lane >> 4;
+  float4v y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int t = 0; t < n; ++t) {
+    const size_t row = (size_t)(t0 + t) * p.ld + head * kHead;
+    auto four = [&](const void* from, int m) {  // the channels of tile m that this lane has
+      const uint2 v = *(const uint2*)((const uint16_t*)from + row + ChunkState::channel(m, g));
+      float f[4];
+      up2<T>(v.x, f);
+      up2<T>(v.y, f + 2);
+      return float4v{f[0], f[1], f[2], f[3]};
+    };
+    auto over_groups = [](float x) {
+      x += __shfl_xor(x, 16);
+      return x + __shfl_xor(x, 32);
+    };
+    const float v = T::up(((const uint16_t*)p.v)[row + 16 * wave + q]);
+    float u = 0.f, out = 0.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float4v a = four(p.a, m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u = fmaf(st.X[m][i], a[i], u);
+    }
+    u = over_groups(u);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float4v w = four(p.w, m), b = four(p.b, m), k = four(p.k, m), r = four(p.r, m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        st.X[m][i] = fmaf(st.X[m][i], __builtin_amdgcn_exp2f(log2_decay(w[i])), fmaf(u, b[i], v * k[i]));
+        out = fmaf(st.X[m][i], r[i], out);
+      }
+    }
+    out = over_groups(out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t == 4 * g + i) y[i] = out;
+  }
+  return y;
 }
 
 // Takes the state over a chunk.  OUT: Y (row t = 4 g + i, column v = q).  REV:
@@ -549,6 +637,12 @@ __device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], con
   interleave<12, 1, 0>();
   interleave<(12 + (OUT ? 6 : 0)), 0, 4>();
   __builtin_amdgcn_sched_barrier(0);
+  if (OUT)
+    // cut here, between the products, and not where the loop's two entries meet
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) asm volatile("" : "+v"(x[h][n].x), "+v"(x[h][n].y), "+v"(x[h][n].z), "+v"(x[h][n].w));
   return y;
 }
 
@@ -615,42 +709,59 @@ __device__ __forceinline__ void prepare_chunks(const TimeMix& p, int begin, int 
 
 // A walking wave's side: its part of a state over the run, or of the map
 // (values 0).  In the c-th chunk of the walk: before(c) with the state at hand
-// (multiplied by `end` with REV), save(c, U or Z), and out(c, Y) with OUT.
-template <typename T, bool OUT, bool REV, typename Before, typename Save, typename Out>
+// (multiplied by `end` with REV), save(c, U or Z), and, with OUT, out(c, Y) and
+// steps(c), which takes the state over the chunk token by token.
+template <typename T, bool OUT, bool REV, typename Before, typename Save, typename Out, typename Steps>
 __device__ __forceinline__ void walk_chunks(ChunkState& st, int chunks, ChunkLds& sh, int wave, int lane, uint32_t values,
-                                            Before before, Save save, Out out) {
+                                            Before before, Save save, Out out, Steps steps) {
   ChunkHead<T, REV> hd;
   uint4 x[2][3];
-  if (chunks > 0) {
-    wait_for(&sh.ready[0], 1);
-    hd.fetch(sh.ops[0], wave, lane, values);
+  int c = 0;
+  while (c < chunks) {
+    wait_for(&sh.ready[c % kBuffers], c / kBuffers + 1);
+    hd.fetch(sh.ops[c % kBuffers], wave, lane, values);
     if (REV)
 #pragma unroll
       for (int n = 0; n < 4; ++n) st.X[n] *= hd.end[n];
 #pragma unroll
     for (int h = 0; h < 2; ++h) split_half(st, h, x[h]);
-  }
-  for (int c = 0; c < chunks; ++c) {
-    const int n = c + 1;
-    const ChunkOps& o = sh.ops[c % kBuffers];
-    before(c);
-    // looked at early, so that the answer is here when it is needed
-    const int seen = __hip_atomic_load(&sh.ready[n % kBuffers], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-    const float4v y = chunk_step<T, OUT, REV>(
-        st, x, o, hd, lane,
-        [&] {
-          const int want = n < chunks ? n / kBuffers + 1 : 0;
-          if (__builtin_amdgcn_readfirstlane(seen) < want) wait_for(&sh.ready[n % kBuffers], want);
-          asm volatile("" ::: "memory");
-          // (past the last chunk whatever the buffer holds, for nothing)
-          hd.fetch(sh.ops[n % kBuffers], wave, lane, values);
-          if (REV && n >= chunks)
+    bool whole = true;
+    for (; c < chunks; ++c) {
+      if (OUT) {
+        const int odd = __builtin_amdgcn_readfirstlane(hd.odd);
+        if (__builtin_expect(odd != 0, 0) && leaks(st, hd, odd)) {
+          whole = false;
+          break;
+        }
+      }
+      const int n = c + 1;
+      const ChunkOps& o = sh.ops[c % kBuffers];
+      before(c);
+      // looked at early, so that the answer is here when it is needed
+      const int seen = __hip_atomic_load(&sh.ready[n % kBuffers], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      const float4v y = chunk_step<T, OUT, REV>(
+          st, x, o, hd, lane,
+          [&] {
+            const int want = n < chunks ? n / kBuffers + 1 : 0;
+            if (__builtin_amdgcn_readfirstlane(seen) < want) wait_for(&sh.ready[n % kBuffers], want);
+            asm volatile("" ::: "memory");
+            // (past the last chunk whatever the buffer holds, for nothing)
+            hd.fetch(sh.ops[n % kBuffers], wave, lane, values);
+            if (REV && n >= chunks)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) hd.end[i] = float4v{1.f, 1.f, 1.f, 1.f};
-        },
-        [&](float4v u) { save(c, u); });
-    signal(&sh.done[c % kBuffers], lane);
-    if (OUT) out(c, y);
+              for (int i = 0; i < 4; ++i) hd.end[i] = float4v{1.f, 1.f, 1.f, 1.f};
+          },
+          [&](float4v u) { save(c, u); });
+      signal(&sh.done[c % kBuffers], lane);
+      if (OUT) out(c, y);
+    }
+    // out of the loop, so that it costs the others no registers
+    if (!whole) {
+      const float4v y = steps(c);
+      signal(&sh.done[c % kBuffers], lane);
+      out(c, y);
+      ++c;
+    }
   }
 }
 

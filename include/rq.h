@@ -425,7 +425,10 @@ int rq_gemm_int8_acc(const int8_t *xq, int64_t m, const rq_qweight *w, int32_t *
  * r, w, k, v, a, b: [tokens][ld]; y: [tokens][ldy]; states: fp32
  * [nslots][heads][64][64].  The workspace only makes long sequences faster: a
  * call that has too few sequences and heads to fill the GPU cuts them into
- * segments when it holds the segments' states. */
+ * segments when it holds the segments' states.
+ * A value that is not finite reaches what the formulas lead it to: outputs of
+ * the tokens before it stay as they are.  (Only where a state leaves fp32's
+ * range by itself may up to 15 tokens before go with it.) */
 int rq_time_mix(int dtype, const void *r, const void *w, const void *k, const void *v, const void *a, const void *b,
                 int64_t tokens, int64_t heads, int64_t ld, const int32_t *cu, int64_t nseq, const float *state_in,
                 float *state_out, const int32_t *slots, int64_t nslots, void *y, int64_t ldy, void *workspace,
@@ -437,7 +440,9 @@ int rq_time_mix(int dtype, const void *r, const void *w, const void *k, const vo
  * [nseq][heads][64][64] without slots (NULL: zeros).  The workspace holds the
  * states along the sequences: at least rq_time_mix_backward_bytes(tokens,
  * heads, nseq) bytes (host-only; 0 for arguments out of range), else
- * RQ_ERR_WORKSPACE.  (tokens / 16 + nseq) * heads stays below 2^24. */
+ * RQ_ERR_WORKSPACE.  (tokens / 16 + nseq) * heads stays below 2^24.
+ * A value that is not finite may take any gradient of its sequence and head
+ * with it, and none of the others. */
 size_t rq_time_mix_backward_bytes(int64_t tokens, int64_t heads, int64_t nseq);
 int rq_time_mix_backward(int dtype, const void *r, const void *w, const void *k, const void *v, const void *a,
                          const void *b, int64_t tokens, int64_t heads, int64_t ld, const int32_t *cu, int64_t nseq,

@@ -104,3 +104,50 @@ def test_many_wide_rows(lens, width, nmix, code):
     close(din.get(), want["dshift_in"], code, "dshift_in")
     for z, q in ((dg, "dgamma"), (db, "dbeta"), (dm, "dmu")):
         close(z, want[q], code, q)
+
+
+# one value of one row: at a chunk's ends and inside, at the last token, in a
+# partial chunk, in a short sequence, and in a first, a middle and the last
+# segment of a long one
+@pytest.mark.parametrize("code", TYPES, ids=IDS)
+@pytest.mark.parametrize("what", ["r", "w", "k", "v", "a", "b"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("lens,heads,at", [([40], 2, (16, 19, 31, 36, 39)), ([32, 20], 2, (31, 32)), ([10], 2, (4,)),
+                                           ([1030], 1, (5, 700, 1029))], ids=["one", "two", "short", "long"])
+def test_values_that_are_not_finite(lens, heads, at, bad, what, code):
+    """They reach the outputs that the recurrence leads them to, and none of the
+    tokens before."""
+    t, c, n = sum(lens), 64 * heads, len(lens)
+    dev, val, g = mix_inputs(lens, heads, code, c, 73)
+    state = g.standard_normal((n, heads, 64, 64)).astype(np.float32)
+    sd, cu = torch.from_numpy(state).cuda(), offsets(lens)
+    for i in at:
+        say("not finite", lens, what, bad, i, code)
+        d, v = dict(dev, **{what: dev[what].clone()}), dict(val, **{what: val[what].copy()})
+        d[what][i, 5], v[what][i, 5] = bad, bad
+        y, out = Out(t, c, c, code), torch.empty_like(sd)
+        rq.rq_time_mix(code, *(d[q] for q in "rwkvab"), t, heads, c, cu, n, sd, out, None, n, y.ptr(), c)
+        torch.cuda.synchronize()
+        with np.errstate(all="ignore"):
+            wy, ws = mix.time_mix(*(v[q] for q in "rwkvab"), lens, state)
+        for got, want, name in ((y.get(), wy, "y"), (out, ws, "state")):
+            fine = np.isfinite(want)
+            assert np.array_equal(torch.isfinite(got).cpu().numpy(), fine), (name, i)
+            if fine.any():
+                close(got.cpu()[torch.from_numpy(fine)], want[fine], code, name)
+
+
+@pytest.mark.parametrize("code", TYPES, ids=IDS)
+def test_rows_that_are_nowhere_finite(code):
+    """From the first token on that is not finite to the end."""
+    heads, lens = 2, [300]
+    dev, val, g = mix_inputs(lens, heads, code, 128, 74)
+    say("nowhere finite", code)
+    for z in dev.values():
+        z[37:] = float("nan")
+    y = Out(300, 128, 128, code)
+    rq.rq_time_mix(code, *(dev[q] for q in "rwkvab"), 300, heads, 128, None, 1, None, None, None, 0, y.ptr(), 128)
+    torch.cuda.synchronize()
+    wy, _ = mix.time_mix(*(val[q][:37] for q in "rwkvab"), [37])
+    close(y.get()[:37], wy, code, "y")
+    assert bool(torch.isnan(y.get()[37:]).all())
