@@ -92,8 +92,12 @@ __device__ __forceinline__ uint4 pair(uint2 a, uint2 b) { return make_uint4(a.x,
 
 // A product over 16 tokens fills half of an instruction's 32 slots, so two
 // term products go side by side: (a0, a1) with (b0, b0) and so on.  The
-// 16-slot instruction is not used: it takes as long, and its result as the
-// addend of a 32-slot one came out without its last two registers at times.
+// 16-slot instruction takes as long and is not used: in an earlier form of
+// these kernels, where 32-slot instructions went on adding to its results,
+// sums came out without their last two registers, at some timings.  Why is not
+// known; the instruction, the compiler's wait states and that form's own order
+// are all possible.  What is kept to here: a result that another kind of matrix
+// instruction adds to has been read by a vector instruction first (settled).
 __device__ __forceinline__ float4v mul_tokens(const uint2* a, const uint2* b, float4v c) {
   c = mfma32(pair(a[0], a[2]), pair(b[2], b[0]), c);
   c = mfma32(pair(a[0], a[1]), pair(b[1], b[1]), c);
@@ -414,6 +418,18 @@ struct ChunkState {
       for (int i = 0; i < 4; ++i) X[n][i] = channel(n, g) + i == 16 * wave + q ? 1.f : 0.f;
   }
 
+  // Passes the state through vector moves, which wait for whatever wrote it.
+  __device__ __forceinline__ void settled() {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = X[n][i];
+        X[n][i] = dpp<0xe4>(x);  // quad_perm 0,1,2,3: as it is
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
   // S <- S P + G with P, G [64][64] in fp32, on fp32 matrix instructions:
   // register i of tile n is the slot of contraction channel(n, g) + i.
   __device__ __forceinline__ void apply(const float* G, const float* P, int wave, int lane) {
@@ -430,6 +446,7 @@ struct ChunkState {
           to.X[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[(channel(n, g) + i) * kHead], X[n][i], to.X[m], 0, 0, 0);
     }
     *this = to;
+    settled();
   }
 };
 
