@@ -291,6 +291,8 @@ class TimeMix:
         m, c = x.shape
         x, delta, cu, slots = _dense(x, delta, cu, slots)
         full = x if delta is None else torch.empty_like(x)
+        if m == 0:      # empty sequences: what the slots hold stays
+            return full, torch.empty_like(x)
         mixes = torch.empty(len(MIXTURES), m, c, dtype=x.dtype, device=x.device)
         rq.rq_shift_norm(rq.RQ_F16, x, delta, 1.0, m, c, c, cu, n, p["gamma"], p["beta"], NORM_EPS, p["mu"], len(MIXTURES),
                          shift, shift, slots, nslots, None if delta is None else full, mixes, c)

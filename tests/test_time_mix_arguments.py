@@ -91,3 +91,16 @@ def test_serving(name, value, error):
         layer.serve(**given)
     with pytest.raises(ValueError, match="GPU"):
         layer.serve(**SERVE)
+
+
+def test_serving_nothing(monkeypatch):
+    """Empty sequences only: the products take no null addresses, which empty
+    tensors have."""
+    monkeypatch.setattr(tm, "_on_gpu", lambda *ts: None)
+    layer = tm.TimeMix(C, rank=8, device="cpu")
+    layer.quantized = {}
+    shift, state = torch.ones(3, C, dtype=F16), torch.ones(3, 2, 64, 64)
+    for delta in (None, rows(t=0)):
+        full, out = layer.serve(rows(t=0), delta, tm.offsets([0, 0], "cpu"), shift, state, torch.zeros(2, dtype=torch.int32))
+        assert full.shape == out.shape == (0, C) and out.dtype == F16
+    assert bool((shift == 1).all()) and bool((state == 1).all())
