@@ -21,6 +21,8 @@ The layer, with x' = x + delta and six mixtures m_i of its shifted norm:
     kappa   = k k_k, of unit length in each head;   k' = k (1 + (rate - 1) k_a)
     y       = the state recurrence of r, w, k', v, -kappa, kappa rate
     out     = W_o head_gate(y, r, k', v, g)
+It is a model's first layer: RWKV-7's later ones also mix the first layer's v
+into theirs, which is not done here.
 """
 
 import argparse
@@ -322,6 +324,8 @@ def main(argv=None):
     ap.add_argument("--train", type=int, default=1024, help="tokens of the training step's sequence")
     args = ap.parse_args(argv)
     lens = [int(n) for n in args.prompts.split(",")]
+    if min(lens) < 1:
+        ap.error("a prompt has at least one token")
     n = len(lens)
     layer = TimeMix(args.width).quantize()
     shift, state = layer.states(n)
@@ -342,13 +346,13 @@ def main(argv=None):
     layer.serve(x, None, cu, *layer.states(n), slots)                     # loads the kernels
     (_, out), us = timed(lambda: layer.serve(x, None, cu, shift, state, slots))
     print("prompts %s: %.0f us, output rms %.4f" % (args.prompts, us, out.float().pow(2).mean().sqrt()))
-    x = out[cu[1:].long() - 1]
+    x, delta = out[cu[1:].long() - 1], None
     one = offsets([1] * n)
     for i in range(args.tokens):
-        (x, out), us = timed(lambda: layer.serve(x, out if len(out) == n else None, one, shift, state, slots))
+        (x, delta), us = timed(lambda: layer.serve(x, delta, one, shift, state, slots))
     if args.tokens:
         print("decode, %d sequences: %.0f us the last of %d tokens, output rms %.4f"
-              % (n, us, args.tokens, out.float().pow(2).mean().sqrt()))
+              % (n, us, args.tokens, delta.float().pow(2).mean().sqrt()))
     for q in layer.params.values():
         q.requires_grad_(True)
     x, want, cu = rows(args.train), rows(args.train), offsets([args.train])

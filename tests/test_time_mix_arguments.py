@@ -104,3 +104,10 @@ def test_serving_nothing(monkeypatch):
         full, out = layer.serve(rows(t=0), delta, tm.offsets([0, 0], "cpu"), shift, state, torch.zeros(2, dtype=torch.int32))
         assert full.shape == out.shape == (0, C) and out.dtype == F16
     assert bool((shift == 1).all()) and bool((state == 1).all())
+
+
+def test_command_needs_prompts(capsys):
+    """The row after an empty prompt would be another prompt's."""
+    with pytest.raises(SystemExit):
+        tm.main(["--prompts", "3,0"])
+    assert "at least one token" in capsys.readouterr().err
