@@ -291,12 +291,14 @@ hipError_t launch_shift_norm(const ShiftNorm& p, bool bf16, hipStream_t st) {
 // A workgroup walks its run of rows once and finishes row t - 1 when it has
 // p_t; it also reads the row after its run.  One barrier per row sums the four
 // values that three rows in different stages need.  Four channels per thread:
-// the sums of eight parameters' gradients and three rows take most of the 128
-// registers that a workgroup of 1024 has.  The parameter gradients stay in
-// registers over the run and are written as one row of partial sums, which a
-// second kernel adds in order.  Measured: 4096 tokens of width 2048, six
+// the sums of eight parameters' gradients and three rows take more than the 128
+// registers that a workgroup of 1024 has: with six mixtures 18 spills to scratch
+// memory, with eight 62 to 86, above width 4096 (two vectors per thread) some
+// 310 and 450; with one mixture none and 2.  The parameter gradients are held
+// over the run and written as one row of partial sums, which a second kernel
+// adds in order.  Measured: 4096 tokens of width 2048, six
 // mixtures, bf16, 64 us, 2.6 TB/s: two workgroups per compute unit do not hide
-// each row's barrier and sums, and their registers allow no third.
+// each row's barrier, sums and spills, and their registers allow no third.
 template <typename T, int NV, int NM>
 __global__ void __launch_bounds__(1024) shift_norm_back_kernel(ShiftNormBack p, int rows, bool mu_lds) {
   extern __shared__ __align__(16) float mus[];  // mu, if it fits: each row needs all of it

@@ -9,8 +9,9 @@
 // sixteen of them; a row lies across sixteen lanes, four columns each, and the
 // sums S a and S r are four lane rotations.  A run of up to sixteen tokens is
 // staged in LDS as fp32.  For single tokens the states' bytes bound it: 32
-// sequences of 64 heads take 13 us, 5.1 TB/s, what a copy reaches.  For longer
-// ones the chain from token to token does, 0.4 us each.
+// sequences of 64 heads take 13.5 us, 5.1 TB/s (of a pool of 48, part of which
+// the memory-side cache delivers; a large copy reaches 5.0).  For longer ones
+// the chain from token to token does, 0.4 us each.
 //
 // chunk kernel: one workgroup of twelve waves per (sequence or segment, head),
 // sixteen tokens at a time on matrix instructions (time_mix_chunk.h).
@@ -254,11 +255,11 @@ namespace {
 // three times over, twice by itself and once by its map, so cutting pays only
 // from four segments on; they are made to fill the 256 compute units once in
 // each launch, and are at least 128 tokens long.  Measured for one sequence,
-// whole against cut: 32 heads, 512 tokens 43 and 43 us, 1024 78 and 52, 4096
-// 291 and 124; 64 heads, 512 tokens 43 and 45, 1024 79 and 64, 4096 292 and
-// 181; 128 heads in two segments each (without the map), 512 tokens 45 and 57,
-// 4096 297 and 332; 32 heads, 256 tokens 25 and 34.  First segments of 1 to 2
-// times the others' length are within 5% of each other.
+// whole against cut: 32 heads, 256 tokens 29 and 38 us, 512 49 and 44, 1024 91
+// and 52, 4096 340 and 127; 64 heads, 256 tokens 29 and 38, 512 50 and 46, 1024
+// 93 and 66, 4096 341 and 187; 128 heads (want 2) 512 tokens 52 and 54, though
+// 4096 347 and 286.  First segments of 1 to 2 times the others' length are
+// within 5% of each other.
 SegmentSplit segment_split(const TimeMix& p) {
   const SegmentSplit whole = {0, 0, nullptr};
   const int64_t chains = (int64_t)p.seq.nseq * p.heads;
@@ -290,11 +291,12 @@ hipError_t start_chunks(const TimeMix& p, int over, hipStream_t st) {
 
 template <typename T>
 hipError_t start_time_mix(const TimeMix& p, hipStream_t st) {
-  // A chunk workgroup has a compute unit to itself and takes 7.5 us for up to
-  // 16 tokens, a step workgroup 3 + 0.4 us a token, and eight of those share a
-  // unit.  Measured at 32 heads, steps against chunks: 1 sequence of 8 tokens
-  // 6.1 and 7.6 us, of 12 7.6 and 7.7, of 16 9.1 and 7.7; 32 sequences of 4
-  // 9.3 and 28, of 24 30 and 35, of 32 38 and 36.
+  // A chunk workgroup has a compute unit to itself and takes 8.3 us for up to
+  // 16 tokens, a step workgroup 3 + 0.4 us a token, and five of those share a
+  // unit (28 KB of LDS each).  Measured, steps against chunks: 1 sequence of 8
+  // tokens 6.1 and 8.2 us, of 12 7.5 and 8.3, of 16 9.1 and 8.3, with 32 as with
+  // 64 heads; 32 sequences with 32 heads, of 4 tokens 9.8 and 31, of 16 22 and
+  // 31, of 24 31 and 38, of 32 38.5 and 38.9.
   const int64_t chains = (int64_t)p.seq.nseq * p.heads;
   const dim3 grid((unsigned)chains), block(256);
   if (p.seq.tokens <= p.seq.nseq || p.seq.tokens <= 12) {

@@ -56,8 +56,9 @@ struct Chain {
 
 // A workgroup per sequence, head and direction.  Bound by the walk's chain and,
 // where all compute units have one, by what it writes: 4 sequences of 1024
-// tokens and 32 heads take 126 us, without writing the states 94.  Keeping them
-// for every second chunk only (107 us) costs the second launch more.
+// tokens and 32 heads take 124 us.  (When it took 126, 94 without writing the
+// states, and 107 keeping every second chunk's, which cost the second launch
+// more.)
 template <typename T>
 __global__ void __launch_bounds__(64 * kWalkWaves) time_mix_chains_kernel(TimeMixBack b, Chain to) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -180,9 +181,11 @@ __device__ __forceinline__ float entry(const uint4* t, int half, int i) {
 }  // namespace
 
 // The gradients of one chunk and head: four waves, of which wave w takes
-// channels 16 w .. 16 w + 15.  Bound by memory: for 4 sequences of 1024 tokens
-// and 32 heads it reads the 335 MB that the chains leave and moves 220 MB of
-// rows, in 132 us, 4.2 TB/s.
+// channels 16 w .. 16 w + 15.  For 4 sequences of 1024 tokens and 32 heads it
+// reads the 335 MB that the chains leave and moves 220 MB of rows, in 167 us,
+// 3.3 TB/s: its 65 KB of LDS (three terms of every row, so that the gradients
+// are fp32's until they are rounded) leave two workgroups per compute unit to
+// wait for memory.  Three, with two terms, took 134 us.
 template <typename T>
 __global__ void __launch_bounds__(256, 2) time_mix_grad_kernel(TimeMixBack b, Chain from) {
   constexpr int NV = ChunkHead<T, false>::kV;

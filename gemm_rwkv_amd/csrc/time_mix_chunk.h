@@ -586,14 +586,16 @@ __device__ __forceinline__ float4v step_tokens(const TimeMix& p, int head, int t
 // chunk's `end` before that.
 //
 // What bounds it: one wave's chain from state to state.  Its products are
-// about 800 cycles of the matrix unit; cutting results into terms and fetching
-// 26 KB of operands each take about as long, a fetch some 15 cycles of the
+// about 950 cycles of the matrix unit; cutting results into terms and fetching
+// 30 KB of operands each take about as long, a fetch some 15 cycles of the
 // wave's issue and no more than fifteen in flight.  So the three are mixed by
 // hand, instruction by instruction: B, K and `end` between the products with A
 // and R, the next chunk's head (`next`) and the cutting of each half of the
-// new state between the products of its update.  Measured: 0.91 us a chunk by
-// itself, 1.1 beside the preparing waves (which take 0.65 by themselves), 1.3
-// with every compute unit at work, when the clock falls.
+// new state between the products of its update.  Measured: 1.33 us a chunk (one
+// sequence of 4096 tokens, 32 heads), 1.36 with every second compute unit at
+// work (128 heads).  What Y alone takes in two terms in place of three would
+// save 0.1 of it and leave fp16 outputs 1.2e-4 of their norm from those of fp32
+// operations, now 1.2e-5.
 template <typename T, bool OUT, bool REV, typename Next, typename Save>
 __device__ __forceinline__ float4v chunk_step(ChunkState& st, uint4 (*x)[3], const ChunkOps& o, ChunkHead<T, REV>& hd,
                                               int lane, Next next, Save save) {
