@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gemm_rwkv_amd.rq as rq
+from gemm_rwkv_amd import time_mix as tm
 from gpu_helpers import say
 from oracle import mix
 from test_gpu_mix import IDS, TYPES, Out, close, mix_inputs, offsets, rows
@@ -151,3 +152,54 @@ def test_rows_that_are_nowhere_finite(code):
     wy, _ = mix.time_mix(*(val[q][:37] for q in "rwkvab"), [37])
     close(y.get()[:37], wy, code, "y")
     assert bool(torch.isnan(y.get()[37:]).all())
+
+
+def test_gradients_of_other_heads_stay():
+    """A value that is not finite takes no other head's gradients with it."""
+    code, heads, lens = rq.RQ_BF16, 3, [50]
+    dev, _, g = mix_inputs(lens, heads, code, 192, 75)
+    dy, cu = rows(g.standard_normal((50, 192)), code, 192)[0], offsets(lens)
+    say("gradients of other heads")
+    got = []
+    for bad in (False, True):
+        d = {q: z.clone() for q, z in dev.items()}
+        if bad:
+            for z in d.values():
+                z[20:, 64:128] = float("nan")
+        outs = [torch.empty(50, 192, dtype=torch.bfloat16, device="cuda") for _ in range(6)]
+        din = torch.empty(1, heads, 64, 64, device="cuda")
+        rq.rq_time_mix_backward(code, *(d[q] for q in "rwkvab"), 50, heads, 192, cu, 1, None, dy, None, *outs, din)
+        got.append([z[:, q] for z in outs for q in (slice(0, 64), slice(128, 192))] + [din[:, 0], din[:, 2]])
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+def test_torch_functions_on_two_streams():
+    """Calls that cut their sequence and sum partial rows, side by side: as alone."""
+    t, c = 2048, 256
+    dev, _, g = mix_inputs([t], 4, rq.RQ_F16, c, 76)
+    cu, f32 = offsets([t]), dict(dtype=torch.float32, device="cuda")
+    param = [torch.randn(c, **f32) for _ in range(3)]
+    say("torch functions on two streams")
+
+    def go():
+        leaves = [dev[q].clone().requires_grad_(True) for q in "rwkvab"]
+        ps = [p.clone().requires_grad_(True) for p in param]
+        y, st = tm.time_mix(*leaves, cu)
+        out = tm.head_gate(y, *leaves[:1], *leaves[2:5], *ps)
+        _, mixes, _ = tm.shift_norm(out, None, torch.full((6, c), 0.25, **f32), ps[0], ps[1], cu)
+        (mixes.float().sum() + out.float().square().sum() + st.sum()).backward()
+        return [y.detach(), st.detach(), out.detach()] + [z.grad for z in leaves + ps]
+
+    want = go()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(go())
+    torch.cuda.synchronize()
+    for outs in got:
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
