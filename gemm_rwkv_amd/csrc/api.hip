@@ -301,6 +301,9 @@ int quantize_impl(const float* w, const float* imp, const rq_qweight* out, void*
         e = rq::launch_quant_rows_f32(w, n, k, out->format == RQ_FP8_E4M3_CH, out->codes,
                                       (float*)out->scales, flags, s);
         break;
+      case RQ_FP8_E4M3_B128:
+        e = rq::launch_quant_block(w, n, k, out->codes, out->scales, flags, s);
+        break;
       case RQ_F16:
         e = rq::launch_to_f16(w, n * k, (uint16_t*)out->codes, flags, s);
         break;

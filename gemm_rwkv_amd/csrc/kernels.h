@@ -18,6 +18,8 @@ hipError_t launch_quant_rows_f32(const float* w, int64_t n, int64_t k, bool fp8,
                                  float* scales, int* flags, hipStream_t st);
 hipError_t launch_quant_rows_f16(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, bool fp8,
                                  void* codes, float* scales, int* flags, hipStream_t st);
+hipError_t launch_quant_block(const float* w, int64_t n, int64_t k, void* codes, void* scales, int* flags,
+                              hipStream_t st);
 hipError_t launch_to_f16(const float* w, int64_t count, uint16_t* out, int* flags, hipStream_t st);
 hipError_t launch_to_bf16(const float* w, int64_t count, uint16_t* out, int* flags, hipStream_t st);
 

@@ -4,12 +4,15 @@
 #include <hip/hip_runtime.h>
 #include <string.h>
 
+#include "buffers.h"
 #include "kernels.h"
 #include "mix.h"
 #include "rq.h"
 #include "validate.h"
 
+using rqv::Buffers;
 using rqv::Span;
+using rqv::bytes_span;
 
 namespace {
 
@@ -17,81 +20,7 @@ constexpr int64_t kMostWidth = 8192;  // a row is held in the registers of one w
 constexpr int64_t kMostMix = 8;
 constexpr int64_t kMostGrid = (int64_t)1 << 21;  // workgroups of one launch
 
-bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
-
 int hip_status(hipError_t e) { return e == hipSuccess ? RQ_OK : RQ_ERR_HIP; }
-
-Span bytes_span(const void* p, size_t n) {
-  Span s;
-  s.lo = (uintptr_t)p;
-  s.hi = p ? s.lo + n : s.lo;
-  return s;
-}
-
-// What a call reads and writes; no output may overlap anything else, except
-// one that is exactly the input it may replace.
-struct Buffers {
-  static constexpr int kMost = 32;
-  Span in[kMost], out[kMost];
-  const void* same[kMost];  // the input that out[i] may replace
-  int nin = 0, nout = 0;
-  int status = RQ_OK;
-
-  void fail(int st) {
-    if (status == RQ_OK) status = st;
-  }
-  bool pointer(const void* p, bool needed) {
-    if (!p) {
-      if (needed) fail(RQ_ERR_NULL);
-      return false;
-    }
-    if (!rqv::aligned16(p)) fail(RQ_ERR_ALIGN);
-    return true;
-  }
-  void read(const void* p, size_t n, bool needed = true) {
-    if (pointer(p, needed)) in[nin++] = bytes_span(p, n);
-  }
-  void write(const void* p, size_t n, bool needed = true, const void* may_be = nullptr) {
-    if (!pointer(p, needed)) return;
-    same[nout] = may_be;
-    out[nout++] = bytes_span(p, n);
-  }
-  // 16-bit rows [m][ld], n used per row
-  // no rows may be no array: an empty tensor's address is null
-  void read_rows(const void* p, int64_t m, int64_t n, int64_t ld, bool needed = true) {
-    if (pointer(p, needed && m > 0)) in[nin++] = rqv::act_span(p, m, n, ld, 2);
-  }
-  void write_rows(const void* p, int64_t m, int64_t n, int64_t ld, bool needed = true) {
-    if (!pointer(p, needed && m > 0)) return;
-    same[nout] = nullptr;
-    out[nout++] = rqv::act_span(p, m, n, ld, 2);
-  }
-  // int32 indices
-  void read_index(const void* p, int64_t n) {
-    if (!p) return;
-    if (!aligned4(p)) fail(RQ_ERR_ALIGN);
-    in[nin++] = bytes_span(p, (size_t)n * 4);
-  }
-  int check(const void* ws, size_t ws_bytes) {
-    if (status != RQ_OK) return status;
-    for (int i = 0; i < nout; ++i) {
-      for (int j = 0; j < nin; ++j)
-        if (rqv::overlaps(out[i], in[j]) && !(same[i] && in[j].lo == (uintptr_t)same[i] && out[i].lo == in[j].lo))
-          return RQ_ERR_ALIAS;
-      for (int j = i + 1; j < nout; ++j)
-        if (rqv::overlaps(out[i], out[j])) return RQ_ERR_ALIAS;
-    }
-    if (ws) {
-      if (!rqv::aligned16(ws)) return RQ_ERR_ALIGN;
-      const Span w = bytes_span(ws, ws_bytes);
-      for (int i = 0; i < nin; ++i)
-        if (rqv::overlaps(w, in[i])) return RQ_ERR_ALIAS;
-      for (int i = 0; i < nout; ++i)
-        if (rqv::overlaps(w, out[i])) return RQ_ERR_ALIAS;
-    }
-    return RQ_OK;
-  }
-};
 
 // The workspace past the split counters, which these operators leave alone.
 float* parts_of(void* ws, size_t ws_bytes, size_t& n) {

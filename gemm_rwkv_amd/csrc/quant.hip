@@ -14,6 +14,7 @@
 // No fused multiply-add may merge these steps, so contraction is off here.
 #include "device_common.h"
 #include "kernels.h"
+#include "next_token.h"
 
 #pragma clang fp contract(off)
 
@@ -330,6 +331,55 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ i
   if (threadIdx.x == 0) scales[row] = __builtin_bit_cast(float, sb);
 }
 
+// ---------------------------------------------------------------------------
+// e4m3 with one power of two per 128 x 128: a workgroup per block, 64 values a
+// thread.  The scale is the smallest 2^e with absmax <= 448 * 2^e = 1.75 *
+// 2^(8 + e), read off the largest value's exponent and mantissa (never below
+// 2^-127), so every quotient is exact and is rounded once, to the code.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) quant_block_kernel(const float* __restrict__ w, int64_t n, int64_t k,
+                                                          uint32_t* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales, int* __restrict__ flags) {
+  __shared__ float red[4];
+  const int64_t row0 = (int64_t)blockIdx.y * 128;
+  const int64_t col = (int64_t)blockIdx.x * 128 + 4 * (threadIdx.x & 31);
+  float v[16][4];
+  float a = 0.f;
+  bool fin = true;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t row = row0 + 8 * i + (threadIdx.x >> 5);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
+    if (row < n) load4<float>(w + row * k + col, v[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      fin = fin && finite_f32(v[i][j]);
+      a = fmaxf(a, fabsf(v[i][j]));
+    }
+  }
+  if (!fin) raise_flag(flags, 0);
+  a = group_max<64>(a);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
+  __syncthreads();
+  a = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const uint32_t b = __builtin_bit_cast(uint32_t, a);
+  const int byte = max((int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u), 0);
+  const double inv = ldexp(1.0, 127 - byte);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t row = row0 + 8 * i + (threadIdx.x >> 5);
+    uint32_t packed = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) packed |= (uint32_t)f64_to_e4m3((double)v[i][j] * inv) << (8 * j);
+    if (row < n) codes[(row * k + col) >> 2] = packed;
+  }
+  const int64_t blocks = k >> 7, srow = scale_row_bytes(k);
+  if (threadIdx.x == 0) scales[blockIdx.y * srow + blockIdx.x] = (uint8_t)byte;
+  // the row's last word is filled up with zeros
+  if (blockIdx.x == 0 && blocks + threadIdx.x < srow) scales[blockIdx.y * srow + blocks + threadIdx.x] = 0;
+}
+
 // Per-token quantization of fp16 activations in one pass: a workgroup per
 // row, each thread loads its NL blocks of 8 halves at once and keeps them in
 // registers through the row's absmax reduction and the coding.  Same codes
@@ -474,6 +524,14 @@ hipError_t launch_quant_rows_f32(const float* w, int64_t n, int64_t k, bool fp8,
   else
     hipLaunchKernelGGL((quant_rows_kernel<float, false>), dim3((unsigned)n), dim3(256), 0, st, w, k, k,
                        (uint32_t*)codes, scales, flags);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_block(const float* w, int64_t n, int64_t k, void* codes, void* scales, int* flags,
+                              hipStream_t st) {
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL(quant_block_kernel, dim3((unsigned)(k / 128), (unsigned)((n + 127) / 128)), dim3(256), 0, st, w, n, k,
+                     (uint32_t*)codes, (uint8_t*)scales, flags);
   return hipGetLastError();
 }
 

@@ -24,6 +24,7 @@ int check_format(int format, int group) {
     case RQ_I8_CH:
     case RQ_F16:
     case RQ_BF16:
+    case RQ_FP8_E4M3_B128:
       return RQ_OK;
     default:
       return RQ_ERR_FORMAT;
@@ -50,6 +51,8 @@ int check_shape(int format, int group, int64_t n, int64_t k) {
       return (k % 8 == 0) ? RQ_OK : RQ_ERR_SHAPE;
     case RQ_BF16:
       return (k % 32 == 0) ? RQ_OK : RQ_ERR_SHAPE;
+    case RQ_FP8_E4M3_B128:
+      return (k % 128 == 0) ? RQ_OK : RQ_ERR_SHAPE;
   }
   return RQ_ERR_FORMAT;
 }
@@ -89,6 +92,10 @@ int weight_bytes(int format, int group, int64_t n, int64_t k, size_t* codes, siz
     case RQ_F16:
     case RQ_BF16:
       c = N * K * 2;
+      break;
+    case RQ_FP8_E4M3_B128:
+      c = N * K;
+      s = (N + 127) / 128 * (4 * ((K + 511) / 512));
       break;
   }
   if (codes) *codes = c;

@@ -38,6 +38,10 @@ RQ_F16 = 6
 RQ_W5_SYM = 7
 RQ_W6_SYM = 8
 RQ_BF16 = 9
+RQ_F32 = 10
+RQ_FP8_E4M3_B128 = 11
+
+RQ_NORM_NONE, RQ_NORM_RMS, RQ_NORM_LAYER = range(3)
 
 # every symbol include/rq.h declares
 EXPORTS = (
@@ -48,6 +52,7 @@ EXPORTS = (
     "rq_gemm_w4", "rq_quantize_aw", "rq_workspace_bytes", "rq_gemm_small_m_noalloc", "rq_stream_read",
     "rq_proxy", "rq_plan_small_m", "rq_time_mix", "rq_time_mix_backward", "rq_time_mix_backward_bytes",
     "rq_shift_norm", "rq_shift_norm_backward", "rq_head_gate", "rq_head_gate_backward",
+    "rq_norm_quantize", "rq_gemm_fp8_block", "rq_sample",
 )
 
 # rq_plan.kernel
@@ -113,6 +118,9 @@ def lib():
                                        [vp] * 9 + [sz, vp], i32),
             "rq_head_gate": ([i32] + [vp] * 5 + [i64] * 3 + [vp, vp, f32, vp, vp, i64, vp], i32),
             "rq_head_gate_backward": ([i32] + [vp] * 5 + [i64] * 3 + [vp, vp, f32] + [vp] * 11 + [sz, vp], i32),
+            "rq_norm_quantize": ([i32, i32, vp, vp, f32, i64, i64, i64, vp, vp, f32, i32, vp, vp, vp, vp], i32),
+            "rq_gemm_fp8_block": ([vp, vp, i64, qp, i32, vp, i64, vp, sz, vp], i32),
+            "rq_sample": ([i32, vp, i64, i64, i64] + [vp] * 8, i32),
         }
         for name in ("rq_gemv_w4g16", "rq_gemv_w4g32", "rq_gemv_w4g64", "rq_gemv_w8g16",
                      "rq_gemv_w8g32", "rq_gemv_w8g64", "rq_gemv_w4sb256", "rq_gemv_f16"):
@@ -480,6 +488,48 @@ def rq_head_gate_backward(dtype, y, r, k, v, g, tokens, heads, ld, gamma, beta, 
                                      _ptr(dg), _ptr(dgamma), _ptr(dbeta), _ptr(du), *_ws(ws), _stream(stream))
     _check(st, "rq_head_gate_backward")
     return dy
+
+
+# --------------------------------------------------------------------------
+# from the last residual to the next token
+# --------------------------------------------------------------------------
+
+
+def block_scale_row(k):
+    """Bytes of one row of block scales of RQ_FP8_E4M3_B128: one per 128 of k,
+    in words of four."""
+    return 4 * -(-k // 512)
+
+
+def rq_norm_quantize(dtype, norm, x, delta, alpha, rows, width, ld, gamma, beta, eps, fmt, x_out, codes, scales, stream=None):
+    """x' = x + alpha delta, its norm (RQ_NORM_*), and the normed row as codes
+    and scales of RQ_FP8_E4M3_CH, RQ_I8_CH or RQ_FP8_E4M3_B128.  delta, gamma,
+    beta and x_out may be None."""
+    st = lib().rq_norm_quantize(dtype, norm, _ptr(x), _ptr(delta), alpha, rows, width, ld, _ptr(gamma), _ptr(beta), eps, fmt,
+                                _ptr(x_out), _ptr(codes), _ptr(scales), _stream(stream))
+    if st:
+        raise RqError(st, "rq_norm_quantize")
+    return codes
+
+
+def rq_gemm_fp8_block(xq, sx, m, w, dtype, y, ldy, stream=None, ws=None):
+    """y = x W^T of e4m3 codes with a power of two per row and 128 of k (xq, sx)
+    and per 128 x 128 (w); y in dtype RQ_F16, RQ_BF16 or RQ_F32."""
+    d = w.desc()
+    st = lib().rq_gemm_fp8_block(_ptr(xq), _ptr(sx), m, ctypes.byref(d), dtype, _ptr(y), ldy, *_ws(ws), _stream(stream))
+    if st:
+        raise RqError(st, "rq_gemm_fp8_block")
+    return y
+
+
+def rq_sample(dtype, logits, rows, vocab, ld, temperature, top_k, top_p, min_p, u, token, logprob, stream=None):
+    """One int32 token (and the fp32 logarithm of its probability) per row of
+    logits from the uniform numbers u; the parameters are one value a row or None."""
+    st = lib().rq_sample(dtype, _ptr(logits), rows, vocab, ld, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
+                         _ptr(token), _ptr(logprob), _stream(stream))
+    if st:
+        raise RqError(st, "rq_sample")
+    return token
 
 
 def rq_stream_read(buf, nbytes, sink, stream=None):

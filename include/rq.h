@@ -160,7 +160,9 @@ enum rq_format {
   RQ_F16 = 6,
   RQ_W5_SYM = 7,
   RQ_W6_SYM = 8,
-  RQ_BF16 = 9
+  RQ_BF16 = 9,
+  RQ_F32 = 10, /* fp32: a type of rows only (logits), no weight format */
+  RQ_FP8_E4M3_B128 = 11
 };
 
 /* Host-side descriptor of one quantized weight; the four buffers are device
@@ -494,6 +496,70 @@ int rq_head_gate_backward(int dtype, const void *y, const void *r, const void *k
                           const float *u, const void *dout, void *dy, void *dr, void *dk, void *dv, void *dg,
                           float *dgamma, float *dbeta, float *du, void *workspace, size_t workspace_bytes,
                           void *stream);
+
+/*
+ * From a model's last residual to its next token: the norm that leaves 8-bit
+ * rows, the fp8 product with block scales, and sampling.  The norm and the
+ * product also serve a block's projections over prompts.  Rows, alignment and
+ * determinism are as above; none of these calls allocates or synchronizes.
+ */
+
+/* Residual, norm and quantization of each row, in one pass:
+ *     x' = x + alpha delta                          (delta NULL: x' = x)
+ *     h  = n(x') gamma + beta                       (gamma NULL: ones, beta NULL: zeros)
+ * with n(x') = x' (RQ_NORM_NONE), x' / sqrt(mean x'^2 + eps) (RQ_NORM_RMS) or
+ * (x' - mean) / sqrt(var + eps) (RQ_NORM_LAYER).  h and the sum x' are not
+ * rounded before their use; x_out (may be NULL, may be x) gets x' in `dtype`
+ * (RQ_F16 or RQ_BF16, RQ_ERR_FORMAT otherwise).
+ * x, delta, x_out: [rows][ld], ld % 8 == 0; codes: [rows][width] bytes.
+ * format says which codes and scales:
+ *   RQ_FP8_E4M3_CH, RQ_I8_CH (width % 16 == 0): scales fp32 [rows] =
+ *     fp32(absmax h / 448) or / 127, codes the nearest to h / scale, what
+ *     rq_quantize_act makes of h, for rq_gemm_fp8 and rq_gemm_int8;
+ *   RQ_FP8_E4M3_B128 (width % 128 == 0): scales uint8 [rows][4 *
+ *     ceil(width/512)], one power of two per 128 columns by the rule of the
+ *     weight format, for rq_gemm_fp8_block.
+ * A row (a block of 128 columns) that holds an h which is not finite gets a NaN
+ * scale (0xff) and codes of zero, so that products of it are NaN; a sum of
+ * squares past fp32 counts as not finite.  width <= 16384 (RQ_ERR_SHAPE),
+ * eps >= 0 and norm one of the three (RQ_ERR_VALUE). */
+enum rq_norm { RQ_NORM_NONE = 0, RQ_NORM_RMS = 1, RQ_NORM_LAYER = 2 };
+int rq_norm_quantize(int dtype, int norm, const void *x, const void *delta, float alpha, int64_t rows, int64_t width,
+                     int64_t ld, const float *gamma, const float *beta, float eps, int format, void *x_out,
+                     void *codes, void *scales, void *stream);
+
+/* FP8 x FP8 product with block scales on MFMA:
+ *     y[m][n] = sum_b 2^(ex[m][b] + ew[n/128][b]) sum_{k in block b} xq[m][k] wq[n][k]
+ * over blocks b of 128 k, fp32 accumulation, rounded once to `dtype` (RQ_F16,
+ * RQ_BF16 or RQ_F32) when stored.  xq: e4m3fn [m][k]; sx: their scales, uint8
+ * [m][4 * ceil(k/512)] (what rq_norm_quantize leaves); w: RQ_FP8_E4M3_B128;
+ * y: [m][ldy], ldy >= n.  Any m >= 0 below 2^21, n at most 2^27.  A scale of
+ * 0xff makes what it scales NaN.  With a workspace, products of few tiles cut K
+ * (the split counters at its head are left alone). */
+int rq_gemm_fp8_block(const uint8_t *xq, const uint8_t *sx, int64_t m, const rq_qweight *w, int dtype, void *y,
+                      int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token per row of logits z (dtype RQ_F16, RQ_BF16 or RQ_F32; [rows][ld],
+ * ld >= vocab, ld % 8 == 0).  With w_i = exp((z_i - max z) / temperature), the
+ * tokens of a row in the order of falling z, equal ones by rising index, are
+ * filtered one filter after the other:
+ *   top_k: the first top_k stay (0 or less: all);
+ *   top_p: the shortest prefix that holds at least top_p of the mass left (1 or
+ *          more: all; at least the first stays);
+ *   min_p: those with w_i >= min_p stay (0 or less: all; above 1 counts as 1).
+ * The token is the first of those that stay, by index, whose cumulative mass
+ * exceeds u times their mass, u clamped to [0, 1 - 2^-24].  logprob (may be
+ * NULL) gets the logarithm of its share of that mass.
+ * temperature, top_k, top_p, min_p, u: one value per row (device, 4-byte
+ * aligned); the first four may be NULL (1, and no filter).  A temperature of 0
+ * or less (or NaN) takes the first of the largest logits, with logprob 0.
+ * A NaN logit counts as -inf, NaN in top_p or min_p as no filter, in u as 0; -inf
+ * is never drawn; beside +inf nothing else is.  A row with nothing to draw
+ * gets token -1 and logprob -inf.  Weights and sums are fp64.
+ * rows < 2^21, vocab <= 2^20. */
+int rq_sample(int dtype, const void *logits, int64_t rows, int64_t vocab, int64_t ld, const float *temperature,
+              const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
+              float *logprob, void *stream);
 
 /* Measurement aid: reads `bytes` of device memory at buf (16-byte aligned,
  * bytes % 16 == 0) with 16-byte non-temporal loads spread over every compute
