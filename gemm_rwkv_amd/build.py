@@ -31,10 +31,10 @@ FLAGS = [
 ]
 
 
-# per-source options: the dense GEMM keeps its accumulators in VGPRs (with
+# per-source options: the dense GEMMs keep their accumulators in VGPRs (with
 # them in AGPRs the allocator shuttles them between the two files every
 # k step of the double-buffered loop)
-EXTRA = {"gemm_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("gemm_mfma.hip", "gemm_block.hip")}
 
 
 def _compile(src):

@@ -17,6 +17,8 @@
 // so there the codes are widened to fp16, which holds each of them, their
 // products go through the fp16 instruction, which keeps fp32, and each block's
 // sum is scaled as it joins the row's.
+#include <atomic>
+
 #include "mix.h"
 #include "next_token.h"
 
@@ -45,7 +47,28 @@ __device__ __forceinline__ void put(void* y, size_t at, float v) {
     ((uint16_t*)y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// The E8M0 bytes of a block of w and one of x.
+// Four consecutive outputs of row m from column n on, those that y has.
+template <int OUT>
+__device__ __forceinline__ void put4(const BlockGemm& p, int m, int n, float4v v) {
+  if (m >= p.m || n >= p.n) return;
+  const size_t at = (size_t)m * p.ldy + n;
+  if (n + 4 <= p.n && (p.ldy & 3) == 0) {
+    if constexpr (OUT == OUT_F32) {
+      *(float4v*)((float*)p.y + at) = v;
+    } else {
+      uint2 o;
+      o.x = OUT == OUT_F16 ? F16::down2(v[0], v[1]) : BF16::down2(v[0], v[1]);
+      o.y = OUT == OUT_F16 ? F16::down2(v[2], v[3]) : BF16::down2(v[2], v[3]);
+      *(uint2*)((uint16_t*)p.y + at) = o;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < p.n) put<OUT>(p.y, at + i, v[i]);
+}
+
+// The E8M0 bytes of a block of w and one of x, in the lowest byte.
 struct Scales {
   int w, x;
 };
@@ -60,6 +83,8 @@ __device__ __forceinline__ float4v mfma_block(const uint4* w, const uint4* x, Sc
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(ww + 2 * i), widen8(xx + 2 * i), sum, 0, 0, 0);
+    e.w &= 255;
+    e.x &= 255;
     const float one = e.w == 255 || e.x == 255 ? __builtin_nanf("") : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(__builtin_amdgcn_ldexpf(sum[i], e.w + e.x - 254), one, c[i]);
@@ -71,97 +96,294 @@ __device__ __forceinline__ float4v mfma_block(const uint4* w, const uint4* x, Sc
   }
 }
 
-// Few rows: the weights stream from memory straight into registers.
-//
-// A workgroup has 16 NT rows of w and all of x; its KW waves take the k blocks
-// wave, wave + KW, ... in groups of U whose loads are issued together, and
-// their sums meet in LDS in wave order.  Rows past m or n read the last one:
-// they only reach outputs that are never stored.
-template <int MT, int NT, int KW, int U, int OUT>
-__global__ void __launch_bounds__(64 * KW) gemm_block_stream_kernel(BlockGemm p) {
-  __shared__ float4v red[KW][MT * NT][64];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int r = lane & 15, q = lane >> 4;
-  const int m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * 16 * NT;
-  const int blocks = p.k >> 7;
-  const int srow = (int)scale_row_bytes(p.k);
-  const uint8_t *xs[MT], *ws[NT], *xe[MT], *we[NT];
-#pragma unroll
-  for (int a = 0; a < MT; ++a) {
-    const size_t row = (size_t)min(m0 + 16 * a + r, p.m - 1);
-    xs[a] = p.xq + row * p.k + 16 * q;
-    xe[a] = p.sx + row * srow;
-  }
-#pragma unroll
-  for (int b = 0; b < NT; ++b) {
-    const size_t row = (size_t)min(n0 + 16 * b + r, p.n - 1);
-    ws[b] = p.wq + row * p.k + 16 * q;
-    we[b] = p.sw + (row >> 7) * srow;
-  }
-  float4v acc[MT][NT];
-#pragma unroll
-  for (int a = 0; a < MT; ++a)
-#pragma unroll
-    for (int b = 0; b < NT; ++b) acc[a][b] = float4v{0, 0, 0, 0};
+// One LDS DMA: 16 (4) bytes per lane from g to base + 16 (4) * lane.  Inline
+// assembly, since the compiler cannot tell which LDS bytes a DMA writes and
+// would wait for all of them before any LDS read; it writes no register, and
+// every read of its bytes comes after an explicit wait.
+__device__ __forceinline__ void dma16(const void* g, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const void* g, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
 
-  for (int first = wave; first < blocks; first += KW * U) {
-    uint4 x[U][MT][2], w[U][NT][2];
-    int ex[U][MT], ew[U][NT];
+// Rows in whole lines: a workgroup has 16 TM rows of x and 16 TN of w; its KW
+// waves take the k blocks wave, wave + KW, ... and each covers the whole tile,
+// through two private stages of LDS that DMA fills: an instruction copies 8 rows
+// x 128 bytes, whole lines, where a load in the operands' own layout touches
+// half of each line and gets half of the bytes per clock.  The 16-byte segment s
+// of row r lies at slot s ^ (r % 8), so that the sixteen lanes that LDS serves
+// together read sixteen bank groups.  The scales of the tile's rows come to LDS
+// first.
+template <int TM, int TN, int KW, int OUT>
+__global__ void __launch_bounds__(64 * KW) gemm_block_lines_kernel(BlockGemm p) {
+  constexpr int BM = 16 * TM, BN = 16 * TN, STAGE = (BM + BN) * 128;
+  extern __shared__ uint4 lds4[];
+  uint8_t* const lds = (uint8_t*)lds4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int r = lane & 15, q = lane >> 4;
+  const int m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
+  const int blocks = p.k >> 7, srow = (int)scale_row_bytes(p.k);
+  uint8_t* const sx = lds + KW * 2 * STAGE;  // [BM][srow], then w's [srow]
+
+  const uint8_t* src[2 * (TM + TN)];
+  const int drow = lane >> 3, dslot = lane & 7;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // past the end: the last block again, with its product left out
-      const int kb = min(first + u * KW, blocks - 1);
+  for (int i = 0; i < 2 * (TM + TN); ++i) {
+    const int row = 8 * i + drow;
+    const int seg = (dslot ^ (row & 7)) << 4;
+    src[i] = (i < 2 * TM ? p.xq + (size_t)min(m0 + row, p.m - 1) * p.k : p.wq + (size_t)min(n0 + row - BM, p.n - 1) * p.k) + seg;
+  }
+  const uint32_t ring = lds_address(lds) + wave * 2 * STAGE;
+  auto dma = [&](int stage, int kb) {
 #pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        w[u][b][0] = *(const uint4*)(ws[b] + (size_t)kb * 128);
-        w[u][b][1] = *(const uint4*)(ws[b] + (size_t)kb * 128 + 64);
-        ew[u][b] = we[b][kb];
-      }
+    for (int i = 0; i < 2 * (TM + TN); ++i) dma16(src[i] + (size_t)kb * 128, ring + stage * STAGE + i * 1024);
+  };
+  if (wave < blocks) dma(0, wave);
+  for (int i = tid; i < (BM + 1) * (srow >> 2); i += 64 * KW) {
+    const int row = i / (srow >> 2), at = i - row * (srow >> 2);
+    const uint8_t* from = row < BM ? p.sx + (size_t)min(m0 + row, p.m - 1) * srow : p.sw + (size_t)(n0 >> 7) * srow;
+    ((uint32_t*)sx)[i] = ((const uint32_t*)from)[at];
+  }
+  __syncthreads();
+
+  const int swz = r & 7;
+  const int o0 = r * 128 + ((q ^ swz) << 4), o1 = r * 128 + (((q + 4) ^ swz) << 4);
+  float4v acc[TM][TN];
 #pragma unroll
-      for (int a = 0; a < MT; ++a) {
-        x[u][a][0] = *(const uint4*)(xs[a] + (size_t)kb * 128);
-        x[u][a][1] = *(const uint4*)(xs[a] + (size_t)kb * 128 + 64);
-        ex[u][a] = xe[a][kb];
-      }
+  for (int a = 0; a < TM; ++a)
+#pragma unroll
+    for (int b = 0; b < TN; ++b) acc[a][b] = float4v{0, 0, 0, 0};
+  int stage = 0;
+  for (int kb = wave; kb < blocks; kb += KW, stage ^= 1) {
+    if (kb + KW < blocks) {
+      dma(stage ^ 1, kb + KW);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (TM + TN)) : "memory");  // block kb has landed
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const uint8_t* at = lds + (wave * 2 + stage) * STAGE;
+    uint4 x[TM][2], w[TN][2];
+    int ex[TM];
+#pragma unroll
+    for (int a = 0; a < TM; ++a) {
+      x[a][0] = *(const uint4*)(at + a * 2048 + o0);
+      x[a][1] = *(const uint4*)(at + a * 2048 + o1);
+      ex[a] = sx[(16 * a + r) * srow + kb];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (first + u * KW < blocks)
+    for (int b = 0; b < TN; ++b) {
+      w[b][0] = *(const uint4*)(at + (TM + b) * 2048 + o0);
+      w[b][1] = *(const uint4*)(at + (TM + b) * 2048 + o1);
+    }
+    const int ew = sx[BM * srow + kb];
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+    for (int a = 0; a < TM; ++a)
 #pragma unroll
-          for (int b = 0; b < NT; ++b) acc[a][b] = mfma_block<OUT == OUT_F32>(w[u][b], x[u][a], Scales{ew[u][b], ex[u][a]}, acc[a][b]);
+      for (int b = 0; b < TN; ++b) acc[a][b] = mfma_block<OUT == OUT_F32>(w[b], x[a], Scales{ew, ex[a]}, acc[a][b]);
   }
+  // the waves' sums, one row of tiles at a time, in the stages that are free now
+  float4v(*red)[TN][64] = (float4v(*)[TN][64])lds4;
 #pragma unroll
-  for (int a = 0; a < MT; ++a)
+  for (int a = 0; a < TM; ++a) {
+    __syncthreads();
 #pragma unroll
-    for (int b = 0; b < NT; ++b) red[wave][a * NT + b][lane] = acc[a][b];
-  __syncthreads();
-  for (int t = wave; t < MT * NT; t += KW) {
-    float4v v = red[0][t][lane];
+    for (int b = 0; b < TN; ++b) red[wave][b][lane] = acc[a][b];
+    __syncthreads();
+    for (int b = wave; b < TN; b += KW) {
+      float4v v = red[0][b][lane];
 #pragma unroll
-    for (int w = 1; w < KW; ++w) v += red[w][t][lane];
-    const int m = m0 + (t / NT) * 16 + r;
-    if (m >= p.m) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + (t % NT) * 16 + 4 * q + i;
-      if (n < p.n) put<OUT>(p.y, (size_t)m * p.ldy + n, v[i]);
+      for (int w = 1; w < KW; ++w) v += red[w][b][lane];
+      put4<OUT>(p, m0 + 16 * a + r, n0 + 16 * b + 4 * q, v);
     }
   }
 }
 
-template <int MT, int OUT>
-hipError_t launch_stream(const BlockGemm& p, hipStream_t st) {
-  const dim3 grid((p.n + 15) / 16, (p.m + 16 * MT - 1) / (16 * MT));
-  hipLaunchKernelGGL((gemm_block_stream_kernel<MT, 1, 4, 2, OUT>), grid, dim3(256), 0, st, p);
+// Many rows: a tile of BM = 16 XT WX rows of x and BN = 16 WT WW of w by WX x WW
+// waves, each with XT x WT blocks of 16 x 16 over all of K.  The waves copy every
+// k block together into a ring of NB stages, in whole lines and with the same
+// swizzle, so that it crosses from L2 once per workgroup.
+template <int XT, int WT, int WX, int WW, int NB, int OUT>
+__global__ void __launch_bounds__(64 * WX * WW) gemm_block_tile_kernel(BlockGemm p) {
+  constexpr int WAVES = WX * WW, BM = 16 * XT * WX, BN = 16 * WT * WW;
+  constexpr int STAGE = (BM + BN) * 128, PER = (BM + BN) / 8 / WAVES;
+  static_assert((BM + BN) / 8 % WAVES == 0 && (BM + BN) % 64 == 0, "copies divide over the waves");
+  extern __shared__ uint4 lds4[];
+  uint8_t* const lds = (uint8_t*)lds4;
+  uint32_t* const scales = (uint32_t*)(lds + NB * STAGE);  // [2][BM + BN]: four blocks' bytes each
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = lane & 15, q = lane >> 4;
+  const int m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
+  const int blocks = p.k >> 7, srow = (int)scale_row_bytes(p.k);
+  const int wx = wave / WW, ww = wave % WW;
+
+  const uint8_t* src[PER];
+  const int drow = lane >> 3, dslot = lane & 7;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int row = 8 * (wave * PER + i) + drow;
+    const int seg = (dslot ^ (row & 7)) << 4;
+    src[i] = (row < BM ? p.xq + (size_t)min(m0 + row, p.m - 1) * p.k : p.wq + (size_t)min(n0 + row - BM, p.n - 1) * p.k) + seg;
+  }
+  // and the scales of 64 rows at a time
+  constexpr int PARTS = (BM + BN) / 64, EACH = (PARTS + WAVES - 1) / WAVES;
+  const uint8_t* ssrc[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int row = 64 * (wave + i * WAVES) + lane;
+    ssrc[i] = row < BM ? p.sx + (size_t)min(m0 + row, p.m - 1) * srow : p.sw + (size_t)(min(n0 + row - BM, p.n - 1) >> 7) * srow;
+  }
+  const uint32_t base = lds_address(lds), sbase = base + NB * STAGE;
+  auto dma = [&](int kb) {
+    if ((kb & 3) == 0)
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        if (wave + i * WAVES < PARTS) dma4(ssrc[i] + kb, sbase + ((kb >> 2) & 1) * 4 * (BM + BN) + (wave + i * WAVES) * 256);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) dma16(src[i] + (size_t)kb * 128, base + (kb % NB) * STAGE + (wave * PER + i) * 1024);
+  };
+
+  const int swz = r & 7;
+  const int o0 = r * 128 + ((q ^ swz) << 4), o1 = r * 128 + (((q + 4) ^ swz) << 4);
+  float4v acc[XT][WT];
+#pragma unroll
+  for (int a = 0; a < XT; ++a)
+#pragma unroll
+    for (int b = 0; b < WT; ++b) acc[a][b] = float4v{0, 0, 0, 0};
+  int ex[XT], ew[WT];
+
+#pragma unroll
+  for (int j = 0; j < NB - 1; ++j)
+    if (j < blocks) dma(j);
+  for (int kb = 0; kb < blocks; ++kb) {
+    // at most the blocks behind the next may still be on their way
+    if (NB > 2 && kb + NB - 2 < blocks)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NB - 2) * PER) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();  // every wave's part of block kb is in; block kb - 1 is done
+    if (kb + NB - 1 < blocks) dma(kb + NB - 1);
+    const uint8_t* at = lds + (kb % NB) * STAGE;
+    const uint8_t* xat = at + wx * XT * 2048;
+    const uint8_t* wat = at + BM * 128 + ww * WT * 2048;
+    if ((kb & 3) == 0) {
+      const uint32_t* s = scales + ((kb >> 2) & 1) * (BM + BN);
+#pragma unroll
+      for (int a = 0; a < XT; ++a) ex[a] = (int)s[(wx * XT + a) * 16 + r];
+#pragma unroll
+      for (int b = 0; b < WT; ++b) ew[b] = (int)s[BM + (ww * WT + b) * 16 + r];
+    }
+    uint4 x[XT][2];
+#pragma unroll
+    for (int a = 0; a < XT; ++a) {
+      x[a][0] = *(const uint4*)(xat + a * 2048 + o0);
+      x[a][1] = *(const uint4*)(xat + a * 2048 + o1);
+    }
+#pragma unroll
+    for (int b = 0; b < WT; ++b) {
+      uint4 w[2];
+      w[0] = *(const uint4*)(wat + b * 2048 + o0);
+      w[1] = *(const uint4*)(wat + b * 2048 + o1);
+#pragma unroll
+      for (int a = 0; a < XT; ++a) acc[a][b] = mfma_block<OUT == OUT_F32>(w, x[a], Scales{ew[b], ex[a]}, acc[a][b]);
+    }
+#pragma unroll
+    for (int a = 0; a < XT; ++a) ex[a] = (int)((uint32_t)ex[a] >> 8);
+#pragma unroll
+    for (int b = 0; b < WT; ++b) ew[b] = (int)((uint32_t)ew[b] >> 8);
+  }
+#pragma unroll
+  for (int a = 0; a < XT; ++a)
+#pragma unroll
+    for (int b = 0; b < WT; ++b) put4<OUT>(p, m0 + (wx * XT + a) * 16 + r, n0 + (ww * WT + b) * 16 + 4 * q, acc[a][b]);
+}
+
+constexpr size_t kLds = 160 << 10;
+
+// LDS past 64 KB is asked for once per kernel and device.
+template <typename K>
+bool allow_lds(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != hipSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+int64_t tiles(const BlockGemm& p, int rows, int cols) {
+  return (int64_t)((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols);
+}
+
+template <int TM, int TN, int KW>
+constexpr size_t lines_lds(int64_t k) {
+  return (size_t)KW * 2 * 16 * (TM + TN) * 128 + (16 * TM + 1) * (size_t)scale_row_bytes(k);
+}
+template <int TM, int TN, int KW, int OUT>
+hipError_t launch_lines(const BlockGemm& p, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (!allow_lds(gemm_block_lines_kernel<TM, TN, KW, OUT>, kLds, done)) return hipErrorInvalidConfiguration;
+  const dim3 grid((p.n + 16 * TN - 1) / (16 * TN), (p.m + 16 * TM - 1) / (16 * TM));
+  hipLaunchKernelGGL((gemm_block_lines_kernel<TM, TN, KW, OUT>), grid, dim3(64 * KW), (lines_lds<TM, TN, KW>(p.k)), st, p);
   return hipGetLastError();
 }
 
+template <int XT, int WT, int WX, int WW, int NB, int OUT>
+hipError_t launch_tile(const BlockGemm& p, hipStream_t st) {
+  constexpr int BM = 16 * XT * WX, BN = 16 * WT * WW;
+  constexpr size_t lds = (size_t)NB * (BM + BN) * 128 + 8 * (BM + BN);
+  static_assert(lds <= kLds, "the ring fits LDS");
+  static std::atomic<uint64_t> done{0};
+  if (!allow_lds(gemm_block_tile_kernel<XT, WT, WX, WW, NB, OUT>, lds, done)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((gemm_block_tile_kernel<XT, WT, WX, WW, NB, OUT>), dim3((p.n + BN - 1) / BN, (p.m + BM - 1) / BM),
+                     dim3(64 * WX * WW), lds, st, p);
+  return hipGetLastError();
+}
+
+// The largest tile that still gives most of the 256 compute units one.  Measured
+// in us on both sides of each border (m x n x k, 16-bit y):
+//   16 x 16, waves 8, or 16 x 32, waves 4, for up to 16 rows: 16 x 16384 x 4096
+//     15.9 and 16.0, 16 x 65536 x 4096 44.6 and 41.6, 16 x 2048 x 2048 3.5 and 3.9;
+//   32 x 16 or 32 x 32: 64 x 2048 x 2048 (256 or 128 tiles) 4.2 and 4.6, 64 x 4096
+//     x 4096 (512 or 256) 9.8 and 8.6;
+//   32 x 32 or 32 x 64: 64 x 4096 x 4096 (256 or 128) 8.6 and 10.6, 128 x 4096 x
+//     4096 (512 or 256) 11.3 and 10.8, 32 x 10240 x 2560 (320 or 160) 10.4 and 9.6;
+//   32 x 64 or 64 x 64: 128 x 4096 x 4096 (256 or 128) 10.8 and 13.2, 256 x 4096 x
+//     4096 (512 or 256) 17.2 and 13.2, 64 x 10240 x 2560 (320 or 160) 12.7 and 11.8;
+//   64 x 64 or 128 x 128: 128 x 8192 x 2048 (256 or 64) 9.2 and 13.6, 200 x 8192 x
+//     2048 (512 or 128) 14.9 and 13.1, 512 x 4096 x 4096 (512 or 128) 22.4 and 21.9;
+//     with up to 64 rows the larger one is half empty: 64 x 16384 x 4096 19.2 and 22;
+//   128 x 128 with four stages or, two workgroups to a compute unit, with two: 256
+//     x 16384 x 4096 (256) 26.2 and 34.9, 512 x 16384 x 4096 (512) 46 and 39;
+//   128 x 128 or 256 x 256: 1000 x 10240 x 2560 (640 or 160) 41 and 40..48, 1024 x
+//     16384 x 4096 (1024 or 256) 71..75 and 60..68.
+// A y in fp32 does twice the matrix work, and past 64 x 64 it always takes 128 x
+// 128 in two stages: 512 x 4096 x 4096 (128 tiles) 46, in tiles of 64 x 64 32, 200
+// x 10240 x 2560 (160) 31.5 and 33, 1000 x 16384 x 4096 150 (four stages 183).
+// Scales of a k so long that they do not fit LDS beside the stages go with the
+// 128 x 128 tile too, which takes four blocks' at a time.
 template <int OUT>
 hipError_t launch_out(const BlockGemm& p, hipStream_t st) {
-  if (p.m <= 16) return launch_stream<1, OUT>(p, st);
-  return launch_stream<4, OUT>(p, st);
+  constexpr bool F32OUT = OUT == OUT_F32;
+  const int64_t t128 = tiles(p, 128, 128);
+  const bool fits = lines_lds<4, 4, 4>(p.k) <= kLds && lines_lds<1, 1, 8>(p.k) <= kLds;
+  if (!fits || (p.m > 64 && t128 >= (F32OUT ? 160 : 128))) {
+    if constexpr (F32OUT) {
+      return launch_tile<4, 4, 2, 2, 2, OUT>(p, st);
+    } else {
+      if (tiles(p, 256, 256) >= 192) return launch_tile<4, 4, 4, 4, 2, OUT>(p, st);
+      return t128 > 256 ? launch_tile<4, 2, 2, 4, 2, OUT>(p, st) : launch_tile<4, 2, 2, 4, 4, OUT>(p, st);
+    }
+  }
+  if (p.m <= 16) return tiles(p, 16, 16) < 2048 ? launch_lines<1, 1, 8, OUT>(p, st) : launch_lines<1, 2, 4, OUT>(p, st);
+  if (p.m > 32 && tiles(p, 64, 64) >= 160) return launch_lines<4, 4, 4, OUT>(p, st);
+  if (tiles(p, 32, 64) >= 160) return launch_lines<2, 4, 4, OUT>(p, st);
+  if (tiles(p, 32, 32) >= 160) return launch_lines<2, 2, 4, OUT>(p, st);
+  return launch_lines<2, 1, 4, OUT>(p, st);
 }
 
 }  // namespace

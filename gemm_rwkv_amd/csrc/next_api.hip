@@ -4,7 +4,6 @@
 #include <string.h>
 
 #include "buffers.h"
-#include "kernels.h"
 #include "next_token.h"
 #include "rq.h"
 #include "validate.h"
@@ -81,7 +80,7 @@ int rq_norm_quantize(int dtype, int norm, const void* x, const void* delta, floa
 }
 
 int rq_gemm_fp8_block(const uint8_t* xq, const uint8_t* sx, int64_t m, const rq_qweight* w, int dtype, void* y,
-                      int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+                      int64_t ldy, void* stream) {
   int st = rqv::check_weight(w);
   if (st != RQ_OK) return st;
   if (w->format != RQ_FP8_E4M3_B128) return RQ_ERR_FORMAT;
@@ -98,7 +97,7 @@ int rq_gemm_fp8_block(const uint8_t* xq, const uint8_t* sx, int64_t m, const rq_
   io.read(xq, (size_t)m * w->k, m > 0);
   io.read(sx, (size_t)m * rq::scale_row_bytes(w->k), m > 0);
   io.write(y, m > 0 ? (size_t)((m - 1) * ldy + w->n) * elem : 0, m > 0 && w->n > 0);
-  if ((st = io.check(workspace, workspace_bytes)) != RQ_OK) return st;
+  if ((st = io.check(nullptr, 0)) != RQ_OK) return st;
   if (m == 0 || w->n == 0) return RQ_OK;
   rq::BlockGemm p;
   memset(&p, 0, sizeof(p));
@@ -111,10 +110,6 @@ int rq_gemm_fp8_block(const uint8_t* xq, const uint8_t* sx, int64_t m, const rq_
   p.n = (int)w->n;
   p.k = (int)w->k;
   p.ldy = (int)ldy;
-  if (workspace && workspace_bytes > rq::kSplitCounterBytes) {
-    p.parts = (float*)((uint8_t*)workspace + rq::kSplitCounterBytes);
-    p.parts_bytes = workspace_bytes - rq::kSplitCounterBytes;
-  }
   return hip_status(rq::launch_gemm_block(p, out, (hipStream_t)stream));
 }
 

@@ -42,8 +42,6 @@ struct BlockGemm {
   const uint8_t* sw;  // [ceil(n / 128)][scale_row_bytes(k)]
   void* y;            // [m][ldy]
   int m, n, k, ldy;
-  float* parts;       // workspace for partial sums, or null
-  size_t parts_bytes;
 };
 hipError_t launch_gemm_block(const BlockGemm& p, int out, hipStream_t st);
 

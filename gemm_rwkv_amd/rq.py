@@ -119,7 +119,7 @@ def lib():
             "rq_head_gate": ([i32] + [vp] * 5 + [i64] * 3 + [vp, vp, f32, vp, vp, i64, vp], i32),
             "rq_head_gate_backward": ([i32] + [vp] * 5 + [i64] * 3 + [vp, vp, f32] + [vp] * 11 + [sz, vp], i32),
             "rq_norm_quantize": ([i32, i32, vp, vp, f32, i64, i64, i64, vp, vp, f32, i32, vp, vp, vp, vp], i32),
-            "rq_gemm_fp8_block": ([vp, vp, i64, qp, i32, vp, i64, vp, sz, vp], i32),
+            "rq_gemm_fp8_block": ([vp, vp, i64, qp, i32, vp, i64, vp], i32),
             "rq_sample": ([i32, vp, i64, i64, i64] + [vp] * 8, i32),
         }
         for name in ("rq_gemv_w4g16", "rq_gemv_w4g32", "rq_gemv_w4g64", "rq_gemv_w8g16",
@@ -512,11 +512,11 @@ def rq_norm_quantize(dtype, norm, x, delta, alpha, rows, width, ld, gamma, beta,
     return codes
 
 
-def rq_gemm_fp8_block(xq, sx, m, w, dtype, y, ldy, stream=None, ws=None):
+def rq_gemm_fp8_block(xq, sx, m, w, dtype, y, ldy, stream=None):
     """y = x W^T of e4m3 codes with a power of two per row and 128 of k (xq, sx)
     and per 128 x 128 (w); y in dtype RQ_F16, RQ_BF16 or RQ_F32."""
     d = w.desc()
-    st = lib().rq_gemm_fp8_block(_ptr(xq), _ptr(sx), m, ctypes.byref(d), dtype, _ptr(y), ldy, *_ws(ws), _stream(stream))
+    st = lib().rq_gemm_fp8_block(_ptr(xq), _ptr(sx), m, ctypes.byref(d), dtype, _ptr(y), ldy, _stream(stream))
     if st:
         raise RqError(st, "rq_gemm_fp8_block")
     return y

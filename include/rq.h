@@ -534,10 +534,12 @@ int rq_norm_quantize(int dtype, int norm, const void *x, const void *delta, floa
  * RQ_BF16 or RQ_F32) when stored.  xq: e4m3fn [m][k]; sx: their scales, uint8
  * [m][4 * ceil(k/512)] (what rq_norm_quantize leaves); w: RQ_FP8_E4M3_B128;
  * y: [m][ldy], ldy >= n.  Any m >= 0 below 2^21, n at most 2^27.  A scale of
- * 0xff makes what it scales NaN.  With a workspace, products of few tiles cut K
- * (the split counters at its head are left alone). */
+ * 0xff makes what it scales NaN.  A 16-bit y comes from the fp8 matrix
+ * instruction, which cuts the products of a block 13 binary places below the
+ * largest exponent among them (some 2^-14 of y); a y in fp32 from exact products
+ * and fp32 sums.  No workspace. */
 int rq_gemm_fp8_block(const uint8_t *xq, const uint8_t *sx, int64_t m, const rq_qweight *w, int dtype, void *y,
-                      int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+                      int64_t ldy, void *stream);
 
 /* One token per row of logits z (dtype RQ_F16, RQ_BF16 or RQ_F32; [rows][ld],
  * ld >= vocab, ld % 8 == 0).  With w_i = exp((z_i - max z) / temperature), the

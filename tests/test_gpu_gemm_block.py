@@ -34,14 +34,14 @@ def weight(wq, sw):
     return rq.QWeight(B128, 0, n, k, dev(wq), dev(sw))
 
 
-def run(xq, sx, wq, sw, out, ldy=None, ws=None, stream=None):
+def run(xq, sx, wq, sw, out, ldy=None):
     dt, code, _ = OUTS[out]
     (m, k), n = xq.shape, wq.shape[0]
     ldy = ldy or n
     y = torch.full((m * ldy + 32,), 77.0, dtype=dt, device="cuda")
     x_, s_, w_ = dev(xq), dev(sx), weight(wq, sw)
     torch.cuda.synchronize()
-    rq.rq_gemm_fp8_block(x_, s_, m, w_, code, y, ldy, stream=stream, ws=ws)
+    rq.rq_gemm_fp8_block(x_, s_, m, w_, code, y, ldy)
     torch.cuda.synchronize()
     y = y.double().cpu().numpy()
     assert (y[m * ldy:] == 77.0).all()
@@ -70,7 +70,11 @@ def whole(seed, m, n, k):
 SHAPES = [(1, 1, 128), (1, 16, 128), (1, 129, 384), (1, 2048, 2048), (2, 15, 256), (3, 1000, 640), (15, 17, 1152), (16, 128, 768),
           (17, 130, 512), (31, 257, 1280), (33, 64, 2048), (48, 520, 384), (64, 1000, 256), (65, 128, 768), (100, 300, 1024),
           (127, 129, 128), (128, 256, 4096), (129, 1100, 384), (200, 2050, 768), (255, 255, 512), (257, 513, 896),
-          (300, 64, 2560), (513, 384, 640), (1000, 1500, 256), (32, 8200, 1024), (5, 4096, 8192)]
+          (300, 64, 2560), (513, 384, 640), (1000, 1500, 256), (32, 8200, 1024), (5, 4096, 8192),
+          # either side of each tile's border, and more than one round of tiles
+          (16, 32768, 128), (16, 32752, 256), (17, 2560, 384), (40, 5130, 256), (33, 10300, 384), (70, 8100, 256), (64, 20000, 128),
+          (130, 8200, 384), (260, 11000, 256), (257, 16400, 640), (1030, 11000, 384), (3100, 4100, 128), (2, 200, 65664), (70, 130, 65536),
+          (1, 33, 131072), (129, 1, 1024)]
 
 
 @pytest.mark.parametrize("out", OUTS)
@@ -81,18 +85,17 @@ def test_whole_numbers(m, n, k, out):
     assert np.array_equal(run(xq, sx, wq, sw, out), to_out(want, out))
 
 
-@pytest.mark.parametrize("ws", [None, False])
 @pytest.mark.parametrize("out", OUTS)
 @pytest.mark.parametrize("m,n,k", [(1, 300, 2048), (9, 100, 1152), (32, 1000, 768), (50, 129, 640), (128, 200, 2560), (300, 600, 1024),
                                    (40, 2048, 8192)])
-def test_any_codes(m, n, k, out, ws):
+def test_any_codes(m, n, k, out):
     g = np.random.default_rng(m + n)
     x = g.standard_normal((m, k)) * (1 + 30 * (g.random(k) < 0.01))
     x[m // 2, :128] = 0
     xq, sx = nt.quantize_rows(x, nt.FP8_BLOCK)
     wq, sw = nt.quantize_weight(g.standard_normal((n, k)) * k ** -0.5 * np.exp(g.standard_normal((n, 1))))
     want, size = nt.product(xq, sx, wq, sw)
-    got = run(xq, sx, wq, sw, out, ldy=n + 3, ws=ws)
+    got = run(xq, sx, wq, sw, out, ldy=n + 3)
     if out == "f32":
         bound = k * 2.0 ** -24 * size
     else:
@@ -157,23 +160,22 @@ def test_weight_quantizer(n, k):
 
 @pytest.mark.parametrize("m,n,k", [(1, 2048, 2048), (200, 512, 2048), (300, 1500, 512)])
 def test_streams_and_graphs(m, n, k):
-    """Two calls at once on streams and workspaces of their own, and a captured one replayed on new inputs."""
+    """Two calls at once on streams of their own, and a captured one replayed on new inputs."""
     sets = [whole(s, m, n, k) for s in (1, 2)]
     wants = [to_out(nt.product(*s)[0], "f16") for s in sets]
-    bufs = [[dev(s[0]), dev(s[1]), weight(s[2], s[3]), torch.zeros(m, n, dtype=torch.float16, device="cuda"),
-             torch.zeros(rq.rq_workspace_bytes(), dtype=torch.uint8, device="cuda")] for s in sets]
+    bufs = [[dev(s[0]), dev(s[1]), weight(s[2], s[3]), torch.zeros(m, n, dtype=torch.float16, device="cuda")] for s in sets]
     streams = [torch.cuda.Stream() for _ in sets]
     torch.cuda.synchronize()
     for _ in range(5):
         for b, st in zip(bufs, streams):
-            rq.rq_gemm_fp8_block(b[0], b[1], m, b[2], rq.RQ_F16, b[3], n, stream=st, ws=b[4])
+            rq.rq_gemm_fp8_block(b[0], b[1], m, b[2], rq.RQ_F16, b[3], n, stream=st)
     torch.cuda.synchronize()
     for b, want in zip(bufs, wants):
         assert np.array_equal(b[3].double().cpu().numpy(), want)
     b, other = bufs
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        rq.rq_gemm_fp8_block(b[0], b[1], m, b[2], rq.RQ_F16, b[3], n, ws=b[4])
+        rq.rq_gemm_fp8_block(b[0], b[1], m, b[2], rq.RQ_F16, b[3], n)
     for i in range(4):
         src = sets[i % 2]
         b[0].copy_(dev(src[0]))
