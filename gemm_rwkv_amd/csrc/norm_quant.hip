@@ -15,6 +15,10 @@
 // stay in registers over the run, and the next row is on its way while this
 // one is reduced.  A block of 128 columns is 16 consecutive lanes, so its
 // scale takes four lane moves and no barrier.
+//
+// h is made in fp64 of an x' in fp32 (exact unless x and alpha delta lie 2^13
+// apart) and of sums in fp64 over the threads' fp32 ones: in fp32 throughout some
+// h in a million came out on the other side of a border between two codes.
 #include "mix.h"
 #include "next_token.h"
 
@@ -22,34 +26,64 @@ namespace rq {
 
 namespace {
 
-// Largest bit pattern over the 16 lanes of a row / the wave.
+// Largest over the 16 lanes of a row / the wave.
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max(v, dpp_u<0x128>(v));
-  v = max(v, dpp_u<0x124>(v));
-  v = max(v, dpp_u<0x122>(v));
-  v = max(v, dpp_u<0x121>(v));
+template <int CTRL>
+__device__ __forceinline__ uint64_t moved(uint64_t v) {
+  return (uint64_t)moved<CTRL>((uint32_t)(v >> 32)) << 32 | moved<CTRL>((uint32_t)v);
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+  return __builtin_bit_cast(double, moved<CTRL>(__builtin_bit_cast(uint64_t, v)));
+}
+template <typename N>
+__device__ __forceinline__ N row_max(N v) {
+  v = max(v, moved<0x128>(v));  // row_ror 8, 4, 2, 1
+  v = max(v, moved<0x124>(v));
+  v = max(v, moved<0x122>(v));
+  v = max(v, moved<0x121>(v));
   return v;
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   v = row_max(v);
-  v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-  return max(v, (uint32_t)__shfl_xor((int)v, 32));
+  v = max(v, (uint64_t)__shfl_xor((unsigned long long)v, 16));
+  return max(v, (uint64_t)__shfl_xor((unsigned long long)v, 32));
+}
+__device__ __forceinline__ double sum64(double v) {
+  v += moved<0x128>(v);
+  v += moved<0x124>(v);
+  v += moved<0x122>(v);
+  v += moved<0x121>(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// 1 / sqrt(v) to 2^-42, of a first value in fp32 (the library's root and quotient
+// in fp64 would be some hundred instructions that a row waits for)
+__device__ __forceinline__ double inverse_root(double v) {
+  if (v < 0x1p-100) return 1.0 / sqrt(v);
+  const double y = __builtin_amdgcn_rsqf((float)v);
+  return __builtin_fma(y * 0.5, __builtin_fma(-v * y, y, 1.0), y);
 }
 
-// h / s as a float whose rounding to 8 bits is the rounding of the exact
-// quotient: where the quotient is no float, the one of its two neighbours whose
-// last bit is set, so that no tie arises that is none.  inv: 1 / s.
-__device__ __forceinline__ float quotient(float h, float s, float inv) {
-  const float q0 = h * inv;
-  const float q = __builtin_fmaf(__builtin_fmaf(-q0, s, h), inv, q0);
-  const float left = __builtin_fmaf(-q, s, h);
-  uint32_t b = __builtin_bit_cast(uint32_t, q);
-  if (left != 0.f && !(b & 1u)) b += ((left > 0.f) == (h > 0.f)) ? 1u : ~0u;
-  return __builtin_copysignf(__builtin_bit_cast(float, b), h);  // -0 stays -0
+// The upper half of a double, its last bit set where the lower half is not zero:
+// 20 bits of the value that round to 8-bit codes as all of it does.
+__device__ __forceinline__ uint32_t upper(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return (uint32_t)(b >> 32) | min((uint32_t)b, 1u);
+}
+// 2^-e of it as a float, 0 below 2^-126.
+__device__ __forceinline__ float from_upper(uint32_t u, int e) {
+  const uint32_t a = __builtin_elementwise_sub_sat(u & 0x7fffffffu, (uint32_t)(1023 - 127 + e) << 20);
+  return __builtin_bit_cast(float, a << 3 | (u & 0x80000000u));
+}
+
+// h / s, exact where it is a double.  inv: 1 / s.
+__device__ __forceinline__ double quotient(double h, double s, double inv) {
+  const double q = h * inv;
+  return __builtin_copysign(__builtin_fma(__builtin_fma(-q, s, h), inv, q), h);  // -0 stays -0
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -61,30 +95,40 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
          ((uint32_t)(int)rintf(c) & 255u) << 16 | (uint32_t)(int)rintf(d) << 24;
 }
 
-constexpr uint32_t kInf = 0x7f800000u, kNaN = 0x7fc00000u;
+constexpr uint32_t kNaN = 0x7fc00000u;
+constexpr uint32_t kPastFloat = 0x47f00000u;  // upper half of 2^128: what fp32 cannot say is not finite
+
+// Sums past fp32 (and NaN) make a row not finite: what overflows there must not
+// pass for a large norm.
+__device__ __forceinline__ bool past_float(double sum) { return !(__builtin_fabs(sum) <= 3.4028234663852886e38); }
 
 template <typename T, int NORM, int FMT, int NV>
 __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
   // gamma and beta of up to two vectors stay in registers; rows of four
   // (width above 8192) read them again each time
   constexpr bool KEEP = NV <= 2;
-  __shared__ float sums[2][2][8];
-  __shared__ uint32_t most[2][8];
+  __shared__ double sums[2][2][8];
+  __shared__ uint64_t most[2][8];
   const int tid = threadIdx.x, wave = tid >> 6, waves = blockDim.x >> 6;
   const int vecs = p.width >> 3;
   const int begin = blockIdx.x * run, end = run_end(p.rows, begin, run);
+  const double part = 1.0 / p.width;
   bool on[NV];
-  float gm[KEEP ? NV : 1][8], bt[KEEP ? NV : 1][8];
+  double gm[KEEP ? NV : 1][8], bt[KEEP ? NV : 1][8];
+  auto params = [&](int j, int at) {
+    float g[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.f, b[i] = -0.f;  // -0 + x is x, also for -0
+    if (on[at] && p.gamma) load8f(p.gamma + 8 * (at * blockDim.x + tid), g);
+    if (on[at] && p.beta) load8f(p.beta + 8 * (at * blockDim.x + tid), b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gm[j][i] = g[i], bt[j][i] = b[i];
+  };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int v = j * blockDim.x + tid;
     on[j] = v < vecs;
-    if constexpr (KEEP) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) gm[j][i] = 1.f, bt[j][i] = -0.f;  // -0 + x is x, also for -0
-      if (on[j] && p.gamma) load8f(p.gamma + 8 * v, gm[j]);
-      if (on[j] && p.beta) load8f(p.beta + 8 * v, bt[j]);
-    }
+    if constexpr (KEEP) params(j, j);
   }
   uint4 xr[NV], dr[NV];
   auto fetch = [&](int row) {
@@ -99,6 +143,7 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
   int buf = 0;
   for (int row = begin; row < end; ++row, buf ^= 1) {
     float x[NV][8];
+    double h[FMT == ROW_BLOCK ? 1 : NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       up2<T>(xr[j].x, x[j]);
@@ -119,7 +164,7 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
     if (row + 1 < end) fetch(row + 1);
 
     // statistics: two passes over the registers, sums in a fixed order
-    float mean = 0.f, rstd = 1.f;
+    double mean = 0, rstd = 1;
     if constexpr (NORM == NORM_LAYER) {
       float s = 0.f;
 #pragma unroll
@@ -127,70 +172,72 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
         if (on[j])
 #pragma unroll
           for (int i = 0; i < 8; ++i) s += x[j][i];
-      s = wave_sum(s);
-      if ((tid & 63) == 0) sums[buf][0][wave] = s;
+      const double w = sum64(s);
+      if ((tid & 63) == 0) sums[buf][0][wave] = w;
       __syncthreads();
       for (int w = 0; w < waves; ++w) mean += sums[buf][0][w];
-      mean /= (float)p.width;
+      mean = past_float(mean) ? __builtin_nan("") : mean * part;
     }
     if constexpr (NORM != NORM_NONE) {
       float s = 0.f;
+      const float m = (float)mean;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (on[j])
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[j][i] -= mean;
-            s = __builtin_fmaf(x[j][i], x[j][i], s);
-          }
-      s = wave_sum(s);
-      if ((tid & 63) == 0) sums[buf][1][wave] = s;
+          for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[j][i] - m, x[j][i] - m, s);
+      const double w = sum64(s);
+      if ((tid & 63) == 0) sums[buf][1][wave] = w;
       __syncthreads();
-      float ss = 0.f;
+      double ss = 0;
       for (int w = 0; w < waves; ++w) ss += sums[buf][1][w];
-      // squares past fp32 must not pass for a large norm
-      rstd = finite_f32(ss) ? 1.f / sqrtf(ss / (float)p.width + p.eps) : __builtin_bit_cast(float, kNaN);
+      rstd = past_float(ss) ? __builtin_nan("") : inverse_root(__builtin_fma(ss, part, (double)p.eps));
     }
+    const double shift = -mean * rstd;
     // h, and the largest |h| as a bit pattern (NaN and infinities come out on top)
-    uint32_t top[NV], all = 0;
+    uint64_t all = 0;
+    uint8_t* codes = (uint8_t*)p.codes + (size_t)row * p.width;
+    const int groups = p.width / kBlock, srow = (int)scale_row_bytes(p.width);
+    uint8_t* scales = (uint8_t*)p.scales + (size_t)row * srow;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      top[j] = 0;
-      if (!KEEP) {
+      constexpr bool kBlocks = FMT == ROW_BLOCK;
+      if (!KEEP) params(0, j);
+      double* hj = h[kBlocks ? 0 : j];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gm[0][i] = 1.f, bt[0][i] = -0.f;
-        if (on[j] && p.gamma) load8f(p.gamma + 8 * (j * blockDim.x + tid), gm[0]);
-        if (on[j] && p.beta) load8f(p.beta + 8 * (j * blockDim.x + tid), bt[0]);
+      for (int i = 0; i < 8; ++i) {
+        double n = x[j][i];
+        if constexpr (NORM == NORM_LAYER) n = __builtin_fma(n, rstd, shift);
+        if constexpr (NORM == NORM_RMS) n *= rstd;
+        hj[i] = __builtin_fma(n, gm[KEEP ? j : 0][i], bt[KEEP ? j : 0][i]);
+        if (!kBlocks && on[j]) all = max(all, __builtin_bit_cast(uint64_t, hj[i]) & ~0ull >> 1);
       }
-      if (on[j])
+      if constexpr (FMT == ROW_BLOCK) {
+        uint32_t u[8], t = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[j][i] = __builtin_fmaf(x[j][i] * rstd, gm[KEEP ? j : 0][i], bt[KEEP ? j : 0][i]);
-          top[j] = max(top[j], __builtin_bit_cast(uint32_t, x[j][i]) & 0x7fffffffu);
+          u[i] = upper(hj[i]);
+          t = max(t, u[i] & 0x7fffffffu);
         }
-      all = max(all, top[j]);
-    }
-    uint8_t* codes = (uint8_t*)p.codes + (size_t)row * p.width;
-    if constexpr (FMT == ROW_BLOCK) {
-      const int groups = p.width / kBlock, srow = (int)scale_row_bytes(p.width);
-      uint8_t* scales = (uint8_t*)p.scales + (size_t)row * srow;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t t = row_max(top[j]);
-        const bool bad = t >= kInf;
+        t = row_max(on[j] ? t : 0u);
+        const bool bad = t >= kPastFloat;
         // 448 = 1.75 * 2^8: the exponent of the largest, less 8, and one more
         // where its mantissa exceeds 1.75
-        const int byte = max((int)(t >> 23) - 8 + ((t & 0x7fffffu) > 0x600000u), 0);
-        const float inv = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);
+        const int byte = max((int)(t >> 20) - 1023 + 127 - 8 + ((t & 0xfffffu) > 0xc0000u), 0);
         if (!on[j]) continue;
         const int v = j * blockDim.x + tid;
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = from_upper(u[i], byte - 127);
         uint2 c;
-        c.x = e4m3x4(x[j][0] * inv, x[j][1] * inv, x[j][2] * inv, x[j][3] * inv);
-        c.y = e4m3x4(x[j][4] * inv, x[j][5] * inv, x[j][6] * inv, x[j][7] * inv);
+        c.x = e4m3x4(q[0], q[1], q[2], q[3]);
+        c.y = e4m3x4(q[4], q[5], q[6], q[7]);
         if (bad) c = make_uint2(0, 0);
         *(uint2*)(codes + 8 * v) = c;
         if ((v & 15) == 0) scales[v >> 4] = bad ? 0xff : (uint8_t)byte;
       }
+    }
+    if constexpr (FMT == ROW_BLOCK) {
       if (groups + tid < srow) scales[groups + tid] = 0;
     } else {
       constexpr float kMost = FMT == ROW_FP8 ? 448.f : 127.f;
@@ -199,11 +246,9 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
       __syncthreads();
       all = 0;
       for (int w = 0; w < waves; ++w) all = max(all, most[buf][w]);
-      const bool bad = all >= kInf;
-      const float scale = __builtin_bit_cast(float, all) / kMost;
-      // tiny rows: the quotient's remainder stays a normal number
-      const float up = scale < 0x1p-60f ? 0x1p64f : 1.f;
-      const float s = scale * up, inv = 1.f / s;
+      const bool bad = (uint32_t)(all >> 32) >= kPastFloat;
+      const float scale = (float)(__builtin_bit_cast(double, all) / (double)kMost);
+      const double s = scale, inv = 1.0 / s;
       const bool none = bad || scale == 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -212,7 +257,7 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
         if (!none) {
           float q[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(quotient(x[j][i] * up, s, inv), -kMost), kMost);
+          for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(from_upper(upper(quotient(h[j][i], s, inv)), 0), -kMost), kMost);
           if constexpr (FMT == ROW_FP8) {
             c.x = e4m3x4(q[0], q[1], q[2], q[3]);
             c.y = e4m3x4(q[4], q[5], q[6], q[7]);
