@@ -17,6 +17,12 @@
 // so there the codes are widened to fp16, which holds each of them, their
 // products go through the fp16 instruction, which keeps fp32, and each block's
 // sum is scaled as it joins the row's.
+//
+// Up to some 64 rows the weight's way from HBM bounds it: 32 x 65536 x 4096 into
+// fp32 takes 63 us, 4.4 TB/s.  Past that it is the copies from L2 to LDS, which a
+// compute unit takes at some 41 GB/s whatever their depth, and the matrix
+// instructions: 1024 x 16384 x 4096 takes 61 us (2.25 PFLOP/s), its instructions
+// alone 44 and its copies alone 51.
 #include <atomic>
 
 #include "mix.h"

@@ -558,7 +558,9 @@ int rq_gemm_fp8_block(const uint8_t *xq, const uint8_t *sx, int64_t m, const rq_
  * A NaN logit counts as -inf, NaN in top_p or min_p as no filter, in u as 0; -inf
  * is never drawn; beside +inf nothing else is.  A row with nothing to draw
  * gets token -1 and logprob -inf.  Weights and sums are fp64; a weight below
- * 2^-990 counts as 0.
+ * 2^-990 counts as 0.  top_p's border alone goes by weights rounded to whole
+ * multiples of 2^-s, s = 62 less the bits of vocab but at most 51 (45 for 65536),
+ * so that their sums are the same in any order.
  * rows < 2^21, vocab <= 2^20. */
 int rq_sample(int dtype, const void *logits, int64_t rows, int64_t vocab, int64_t ld, const float *temperature,
               const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
