@@ -758,7 +758,7 @@ struct Row {
     __syncthreads();
     constexpr int kDigit = 12;
     static_assert(1 << kDigit == kBins, "a digit has a bin");
-    while (lo != hi) {
+    for (int digits = 0; lo != hi && digits < (32 + kDigit - 1) / kDigit; ++digits) {
       const int bits = 32 - __builtin_clz(lo ^ hi);
       const int drop = bits > kDigit ? bits - kDigit : 0;
       const uint32_t base = drop + kDigit < 32 ? lo >> (drop + kDigit) << (drop + kDigit) : 0;
@@ -825,23 +825,14 @@ __device__ __forceinline__ int draw(const Row<T, NT>& r, const Sample& p, int ro
     }
   }
   if (n > 0) return r.draw_short(n, want, top_p, want ? -1.0 : goal, least, share, whole);
-  if (least > 0.0) {
-    // the smallest float that weighs enough
-    float x = (float)((double)r.top + log2(least) / r.rate);
-    x = fminf(fmaxf(x, -3.4028235e38f), r.top);
-#pragma unroll 1
-    while (x < r.top && !(r.weight(x) >= least)) x = after(x);
-#pragma unroll 1
-    while (x > -3.4e38f && r.weight(-after(-x)) >= least) x = -after(-x);
-    if (x > cut.z) {
-      cut.z = x;
-      cut.index = 0x7fffffff;
-    }
-  }
-  if (cut.none()) return r.walk([&](float x, int, int) { return r.weight(x); }, -1.0, share, whole);
+  if (cut.none() && !(least > 0.0)) return r.walk([&](float x, int, int) { return r.weight(x); }, -1.0, share, whole);
   const float beyond = after(cut.z);
-  return r.walk([&](float x, int at, int e) { return x >= (at + e <= cut.index ? cut.z : beyond) ? r.weight(x) : 0.0; }, -1.0,
-                share, whole);
+  return r.walk(
+      [&](float x, int at, int e) {
+        const double w = r.weight(x);
+        return x >= (at + e <= cut.index ? cut.z : beyond) && w >= least ? w : 0.0;
+      },
+      -1.0, share, whole);
 }
 
 template <typename T, int NT>

@@ -213,3 +213,19 @@ def test_no_logprob_stream_and_graph():
         go()
         torch.cuda.synchronize()
         assert torch.equal(token, got)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_min_p_where_many_floats_weigh_the_same(dtype):
+    """A min_p at or near 1 beside a largest logit of 0, or a temperature under
+    which any two logits weigh the same, where some 2^30 floats lie between the
+    largest and the first that weighs less; more rows than one launch shape."""
+    for rows, vocab in ((4, 1000), (300, 70)):
+        z = logits_of(3, rows, vocab, dtype, scale=1.0)
+        z[0::4] = 0.0
+        z[1::4] -= z[1::4].amax(1, keepdim=True)
+        T = [1.0, 0.7, 1e30, math.inf] * (rows // 4)
+        u = list(np.random.default_rng(4).random(rows))
+        for m in (1.0, 2.0, 1.0 - 2.0 ** -24, 0.999, 1e-30):
+            check(z, vocab, T=T, m=m, u=u)
+            check(z, vocab, T=T, k=vocab - 1, p=0.9999, m=m, u=u)
