@@ -208,3 +208,44 @@ def test_command_runs(capsys):
     assert nx.main(["--width", "256", "--vocab", "1003", "--prompts", "3,17", "--tokens", "4", "--top-k", "30", "--top-p", "0.9"]) == 0
     said = capsys.readouterr().out.splitlines()
     assert len(said) == 3 and all(0 <= int(t) < 1003 for row in said[1:] for t in row.split())
+
+
+def test_far_rows():
+    """Rows whose logits, or codes, start past 2^31 elements and 2^32 bytes."""
+    say("far rows: logits")
+    base, reps = 440, 75
+    z = torch.empty(base * reps, 65544, dtype=torch.float16, device="cuda")
+    part = rows(2, base, 65544, torch.float16)
+    for i in range(reps):
+        z[i * base:(i + 1) * base] = part
+    u = torch.rand(base, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    want = nx.sample(part[:, :65536], temperature=0.8, top_k=30, u=u)
+    got = nx.sample(z[:, :65536], temperature=0.8, top_k=30, u=u.repeat(reps))
+    assert torch.equal(got[0].view(reps, base), want[0].expand(reps, base))
+    assert torch.equal(got[1].view(reps, base), want[1].expand(reps, base))
+    del z, part, got
+    say("far rows: codes")
+    base, reps = 1000, 263
+    x = rows(3, base, 8192, torch.float16)
+    _, codes, scales = nx.norm_quantize(x)
+    _, far, fscales = nx.norm_quantize(x.repeat(reps, 1))
+    for i in (0, 131, 262):
+        assert torch.equal(far[i * base:(i + 1) * base], codes) and torch.equal(fscales[i * base:(i + 1) * base], scales)
+
+
+def test_calls_at_once_on_two_streams():
+    """Each stream's tokens are those of its rows alone."""
+    head = nx.Head(512, 4001, seed=6).quantize()
+    xs = [rows(s, 40, 512, torch.float16) for s in (1, 2)]
+    hows = [filters(s, 40) for s in (1, 2)]
+    want = [head.next(x, **how) for x, how in zip(xs, hows)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(head.next(xs[i], **hows[i]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for pair in g for a, b in zip(pair, w))
