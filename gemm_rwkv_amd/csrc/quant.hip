@@ -341,8 +341,10 @@ __global__ void __launch_bounds__(256) quant_block_kernel(const float* __restric
                                                           uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales, int* __restrict__ flags) {
   __shared__ float red[4];
-  const int64_t row0 = (int64_t)blockIdx.y * 128;
-  const int64_t col = (int64_t)blockIdx.x * 128 + 4 * (threadIdx.x & 31);
+  // one grid dimension: there may be more than 2^16 blocks of rows
+  const int64_t blocks = k >> 7, rb = blockIdx.x / blocks, kb = blockIdx.x - rb * blocks;
+  const int64_t row0 = rb * 128;
+  const int64_t col = kb * 128 + 4 * (threadIdx.x & 31);
   float v[16][4];
   float a = 0.f;
   bool fin = true;
@@ -374,10 +376,10 @@ __global__ void __launch_bounds__(256) quant_block_kernel(const float* __restric
     for (int j = 0; j < 4; ++j) packed |= (uint32_t)f64_to_e4m3((double)v[i][j] * inv) << (8 * j);
     if (row < n) codes[(row * k + col) >> 2] = packed;
   }
-  const int64_t blocks = k >> 7, srow = scale_row_bytes(k);
-  if (threadIdx.x == 0) scales[blockIdx.y * srow + blockIdx.x] = (uint8_t)byte;
+  const int64_t srow = scale_row_bytes(k);
+  if (threadIdx.x == 0) scales[rb * srow + kb] = (uint8_t)byte;
   // the row's last word is filled up with zeros
-  if (blockIdx.x == 0 && blocks + threadIdx.x < srow) scales[blockIdx.y * srow + blocks + threadIdx.x] = 0;
+  if (kb == 0 && blocks + threadIdx.x < srow) scales[rb * srow + blocks + threadIdx.x] = 0;
 }
 
 // Per-token quantization of fp16 activations in one pass: a workgroup per
@@ -530,7 +532,7 @@ hipError_t launch_quant_rows_f32(const float* w, int64_t n, int64_t k, bool fp8,
 hipError_t launch_quant_block(const float* w, int64_t n, int64_t k, void* codes, void* scales, int* flags,
                               hipStream_t st) {
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(quant_block_kernel, dim3((unsigned)(k / 128), (unsigned)((n + 127) / 128)), dim3(256), 0, st, w, n, k,
+  hipLaunchKernelGGL(quant_block_kernel, dim3((unsigned)(k / 128 * ((n + 127) / 128))), dim3(256), 0, st, w, n, k,
                      (uint32_t*)codes, (uint8_t*)scales, flags);
   return hipGetLastError();
 }

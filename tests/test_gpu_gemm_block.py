@@ -204,3 +204,20 @@ def test_far_offsets():
     torch.cuda.synchronize()
     assert not y[:, :n - 64].any()
     assert np.array_equal(y[:, n - 64:].double().cpu().numpy(), to_out(nt.product(xq, sx, wq, sw)[0], "f16"))
+
+
+def test_weight_quantizer_past_2_16_blocks_of_rows():
+    n, k = 128 * 65600 + 5, 128
+    free, _ = torch.cuda.mem_get_info()
+    if free < 12 << 30:
+        pytest.skip("needs 12 GiB of GPU memory")
+    w = torch.zeros(n, k, device="cuda")
+    g = np.random.default_rng(4)
+    ends = g.standard_normal((133, k)).astype(np.float32)
+    w[:128], w[-133:] = dev(ends[:128]), dev(ends)
+    q = rq.quantize(w, B128)
+    wq, sw = nt.quantize_weight(ends)
+    codes, scales = q.codes[:n * k].view(n, k), q.scales[:-(-n // 128) * 4].view(-1, 4)
+    assert np.array_equal(codes[-133:].cpu().numpy(), wq) and np.array_equal(codes[:128].cpu().numpy(), wq[:128])
+    assert np.array_equal(scales[-2:].cpu().numpy(), sw) and np.array_equal(scales[0].cpu().numpy(), sw[0])
+    assert not codes[128:-133].any() and not scales[1:-2].any()
