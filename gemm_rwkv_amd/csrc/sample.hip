@@ -941,7 +941,10 @@ template <typename T>
 hipError_t launch_type(const Sample& p, hipStream_t st) {
   // Up to a row for each of 256 compute units, the row's own time counts: 16 waves.
   // Past that two workgroups of 8 overlap on a unit (one's reads and barriers with
-  // the other's arithmetic): 509 rows of 50277 take 41 us so and 47 with 16 waves.
+  // the other's arithmetic).  Rows of 65536 in fp16, in us with 8 and 16 waves: 300
+  // rows 42 and 47 with no filter, 27 and 35 with top_k 50, 109 and 95 with top_p
+  // alone, 95 and 74 with a mixture; 509 rows 46 and 51, 31 and 38, 122 and 127, 99
+  // and 94; 900 rows 81 and 96, 53 and 72, 190 and 206, 133 and 145.
   if (p.rows > 256)
     hipLaunchKernelGGL((sample_kernel<T, 512>), dim3(p.rows), dim3(512), 0, st, p);
   else
