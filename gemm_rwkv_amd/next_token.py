@@ -64,7 +64,8 @@ def norm_quantize(x, delta=None, gamma=None, beta=None, norm="layer", eps=NORM_E
 def block_product(codes, scales, w, dtype=torch.float16):
     """[rows][w.n] in `dtype` (float16, bfloat16 or float32), the product of
     norm_quantize's codes and scales with the RQ_FP8_E4M3_B128 weight w.  Its
-    rows lie a multiple of 8 elements apart."""
+    rows lie a multiple of 8 elements apart.  Sums are fp32 where dtype is float32
+    or there are at most 16 rows; else see rq_gemm_fp8_block in rq.h."""
     if dtype not in _CODE_Y:
         raise TypeError("dtype is %s, not float16, bfloat16 or float32" % dtype)
     if w.format != rq.RQ_FP8_E4M3_B128:
