@@ -320,9 +320,11 @@ struct Row {
     return __builtin_bit_cast(unsigned long long, __builtin_fma(weight(x), scale, 0x1p52)) & 0xfffffffffffffull;
   }
 
-  // A logit's class, and what it adds to the class's bin.
+  // A logit's class, and what it adds to the class's bin.  It goes by half the
+  // distance from the top, which fp32 holds whatever two finite logits are.
+  __device__ __forceinline__ float half_below(float x) const { return __builtin_fmaf(-0.5f, x, 0.5f * top); }
   __device__ __forceinline__ int klass_of(float x, float per) const {
-    return per < 3e38f ? (int)fminf((top - x) * per, (float)(kBins - 1)) : x == top ? 0 : 1;
+    return per < 3e38f ? (int)fminf(half_below(x) * per, (float)(kBins - 1)) : x == top ? 0 : 1;
   }
   __device__ __forceinline__ unsigned long long measure(bool mass, float x) const {
     return mass ? units(x) : x > kMinusInf ? 1ull : 0ull;
@@ -626,9 +628,10 @@ struct Row {
   __device__ __forceinline__ int select(bool mass, double amount, float temperature, Cut& cut, double& goal_out) const {
     const int tid = threadIdx.x;
     // classes of equal width, over what can matter: 2^-64 of the best and
-    // more, or every logit
-    const float wide = mass ? fminf(45.f * temperature, top - low) : top - low;
-    const float per = wide > 0.f && wide < 3e38f ? (float)kBins / wide : 0.f;
+    // more, or every logit (in halves, as half_below() is); where that is too
+    // little to divide, two: the largest ones and the others
+    const float wide = mass ? fminf(22.5f * temperature, half_below(low)) : half_below(low);
+    const float per = wide > 0.f ? (float)kBins / wide : kInf;
     const bool flat = !(per < 3e38f);
     const Cut was = cut;
     auto klass = [&](float x) { return klass_of(x, per); };
@@ -667,8 +670,8 @@ struct Row {
     if (tid == 0) shared().count[0] = shared().count[1] = 0;
     __syncthreads();
     // values between which the class lies, past any rounding of klass()
-    const float around = fmaxf(wide, fabsf(top)) * 0x1p-20f;
-    const float below = flat ? kMinusInf : top - ((float)in + 1.f) / per - around;
+    const float around = fmaxf(wide, 0.5f * fabsf(top)) * 0x1p-20f;
+    const float below = flat ? kMinusInf : 2.f * (0.5f * top - ((float)in + 1.f) / per - around);
     float above = kInf;
     bool full = false;
     vectors<1>([&](const float* l, int at) {
@@ -690,7 +693,7 @@ struct Row {
             shared().list.order[half * kList + place] = (unsigned long long)key_of(l[e]) << 32 | (uint32_t)~(at + e);
           if (half == 0 && __ballot(mine && place >= kList)) {
             full = true;
-            if (!flat) above = top - (float)in / per + around;
+            if (!flat) above = 2.f * (0.5f * top - (float)in / per + around);
           }
         }
       }
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(NT, 4) sample_kernel(Sample p) {
   if (tid == 0) {
     p.token[row] = at;
     if (p.logprob) {
-      const float x = r.infinite ? hi : Vec<T>::one(z, at);
+      const float x = r.infinite ? hi : Vec<T>::one(z, max(at, 0));  // (a row with a largest logit has a token)
       p.logprob[row] = (float)log(r.weight(x) / whole);
     }
   }
