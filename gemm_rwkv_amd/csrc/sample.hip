@@ -912,6 +912,7 @@ __global__ void __launch_bounds__(NT, 4) sample_kernel(Sample p) {
     most = most == kInf ? 0.f : kMinusInf;
     const int with = __popcll(__ballot(most == 0.f));
     if ((tid & 63) == 0) s.lanes[tid >> 6] = with;
+    __syncthreads();  // (the row's waves all come here; list_best() reads every wave's number)
     hi = 0.f;
   }
   if (!(lo > kMinusInf)) {  // the smallest finite one
