@@ -16,12 +16,13 @@
 // one is reduced.  A block of 128 columns is 16 consecutive lanes, so its
 // scale takes four lane moves and no barrier.
 //
-// h is made in fp64 of an x' in fp32 (exact unless x and alpha delta lie 2^13
-// apart) and of sums in fp64 over the threads' fp32 ones: in fp32 throughout some
-// h in a million came out on the other side of a border between two codes.
+// h is made in fp64, of an x' in fp64 (exact unless x and alpha delta lie 2^18
+// apart) and of sums in fp64 over the threads' fp32 ones, which take x' in fp32:
+// with an x' or an h in fp32 some h in a million came out on the other side of a
+// border between two codes.
 //
-// 8192 rows of 4096 with residual, layer norm and block scales take 51 us, 4.6
-// TB/s, where a large copy reaches 5.0 (with h in fp32: 47).  A few rows take the
+// 8192 rows of 4096 with residual, layer norm and block scales take 53 us, 4.5
+// TB/s, where a large copy reaches 5.0 (with x' in fp32 52, with h too 47).  A few rows take the
 // latency of their reads and of two reductions: 2.8 us for one of 2048.
 #include "mix.h"
 #include "next_token.h"
@@ -146,14 +147,17 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
   fetch(begin);
   int buf = 0;
   for (int row = begin; row < end; ++row, buf ^= 1) {
-    float x[NV][8];
+    double x[NV][8];
+    float xf[NV][8];  // for the statistics and x_out
     double h[FMT == ROW_BLOCK ? 1 : NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      up2<T>(xr[j].x, x[j]);
-      up2<T>(xr[j].y, x[j] + 2);
-      up2<T>(xr[j].z, x[j] + 4);
-      up2<T>(xr[j].w, x[j] + 6);
+      up2<T>(xr[j].x, xf[j]);
+      up2<T>(xr[j].y, xf[j] + 2);
+      up2<T>(xr[j].z, xf[j] + 4);
+      up2<T>(xr[j].w, xf[j] + 6);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] = xf[j][i];
       if (p.delta) {
         float d[8];
         up2<T>(dr[j].x, d);
@@ -161,9 +165,12 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
         up2<T>(dr[j].z, d + 4);
         up2<T>(dr[j].w, d + 6);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[j][i] = __builtin_fmaf(p.alpha, d[i], x[j][i]);
+        for (int i = 0; i < 8; ++i) {
+          x[j][i] = __builtin_fma((double)p.alpha, (double)d[i], x[j][i]);
+          xf[j][i] = (float)x[j][i];
+        }
       }
-      if (p.x_out && on[j]) store8<T>(p.x_out, (size_t)row * p.ld + 8 * (j * blockDim.x + tid), x[j]);
+      if (p.x_out && on[j]) store8<T>(p.x_out, (size_t)row * p.ld + 8 * (j * blockDim.x + tid), xf[j]);
     }
     if (row + 1 < end) fetch(row + 1);
 
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
       for (int j = 0; j < NV; ++j)
         if (on[j])
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s += x[j][i];
+          for (int i = 0; i < 8; ++i) s += xf[j][i];
       const double w = sum64(s);
       if ((tid & 63) == 0) sums[buf][0][wave] = w;
       __syncthreads();
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
       for (int j = 0; j < NV; ++j)
         if (on[j])
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[j][i] - m, x[j][i] - m, s);
+          for (int i = 0; i < 8; ++i) s = __builtin_fmaf(xf[j][i] - m, xf[j][i] - m, s);
       const double w = sum64(s);
       if ((tid & 63) == 0) sums[buf][1][wave] = w;
       __syncthreads();

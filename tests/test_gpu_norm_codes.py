@@ -1,0 +1,59 @@
+"""Codes of rq_norm_quantize that are those of the 64-bit h, byte for byte.
+
+x' = x + alpha delta has at most 35 bits (24 of alpha, 11 of a value, their lowest
+places less than 2^18 apart), so fp64 holds it.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_rwkv_amd.rq as rq
+from oracle import next_token as nt
+from test_gpu_norm_quant import FORMATS, TYPES, call, rows
+
+pytestmark = pytest.mark.gpu
+
+def quantized(h, fmt):
+    """The oracle's codes and scales, many rows at a time (its scales, then its rounding by table)."""
+    r, c = h.shape
+    if fmt == rq.RQ_FP8_E4M3_B128:
+        most = np.abs(h).reshape(r, -1, 128).max(-1)
+        part, e = np.frexp(most / 448.0)
+        e = np.where(most > 0, np.where(part == 0.5, e - 1, e), -127).clip(-127, 127)
+        scales = np.zeros((r, nt.scale_row(c)), dtype=np.uint8)
+        scales[:, :c // 128] = e + 127
+        q = h * np.exp2(-e.astype(float)).repeat(128, 1)
+    else:
+        scales = (np.abs(h).max(1) / (127.0 if fmt == rq.RQ_I8_CH else 448.0)).astype(np.float32)
+        q = h / scales.astype(float)[:, None]
+        if fmt == rq.RQ_I8_CH:
+            return np.clip(np.rint(q), -127, 127).astype(np.int8).view(np.uint8), scales
+    # to a multiple of a code's step, ties to even; the step of [2^e, 2^(e + 1)) is 2^(e - 3), of all below 2^-6 2^-9
+    step = np.exp2(np.maximum(np.frexp(q)[1] - 1, -6) - 3.0)
+    v = np.minimum(np.abs(np.rint(q / step) * step), 448.0)
+    e = np.maximum(np.frexp(v)[1] - 1, -6)
+    code = np.where(v < 2.0 ** -6, v * 512, (e + 7) * 8 + (v / np.exp2(e.astype(float)) - 1) * 8).astype(np.uint8)
+    return code | (np.signbit(q) * 128).astype(np.uint8), scales
+
+
+def test_quantized_is_the_oracles():
+    g = np.random.default_rng(1)
+    h = g.standard_normal((5, 512)) * np.exp2(g.integers(-20, 20, (5, 1)))
+    h[1] = np.round(g.standard_normal(512) * 16) / 16
+    for fmt in FORMATS:
+        for a, b in zip(quantized(h, fmt), nt.quantize_rows(h, fmt)):
+            assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("alpha", [0.1, 0.7071067811865476, 1.0, -1.0 / 3.0])
+@pytest.mark.parametrize("dtype,m,width", [("f16", 700, 4096), ("bf16", 500, 2560), ("f16", 60, 16384), ("bf16", 90, 8192)])
+def test_sums_with_the_residual(dtype, m, width, alpha, fmt):
+    dt, alpha = TYPES[dtype][0], float(np.float32(alpha))
+    x, delta = rows(m, m, width, dt), rows(m + 1, m, width, dt, 0.7)
+    codes, scales = call(x, delta, alpha, width, rq.RQ_NORM_NONE, None, None, 0.0, fmt)
+    h = x.double().cpu().numpy() + alpha * delta.double().cpu().numpy()
+    want, wscale = quantized(h, fmt)
+    assert np.array_equal(scales, wscale)
+    assert np.array_equal(codes, want), int((codes != want).sum())
