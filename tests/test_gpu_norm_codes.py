@@ -1,7 +1,12 @@
 """Codes of rq_norm_quantize that are those of the 64-bit h, byte for byte.
 
 x' = x + alpha delta has at most 35 bits (24 of alpha, 11 of a value, their lowest
-places less than 2^18 apart), so fp64 holds it.
+places less than 2^18 apart), so fp64 holds it.  With a norm the rows are of whole
+numbers, in pairs of opposite signs for the layer norm, whose sums and sums of
+squares stay below 2^24: fp32 sums of them are exact, and what is left is the error
+of 1 / sqrt and of the products in fp64, 2^-40 of h.  An h in fp32 is off by some
+2^-24 of itself; a border between two e4m3 codes lies within that of one h in 2^20
+or so, so of some millions of values several would get another code.
 """
 
 import numpy as np
@@ -13,6 +18,9 @@ from oracle import next_token as nt
 from test_gpu_norm_quant import FORMATS, TYPES, call, rows
 
 pytestmark = pytest.mark.gpu
+
+EPS = float(np.float32(1e-5))
+
 
 def quantized(h, fmt):
     """The oracle's codes and scales, many rows at a time (its scales, then its rounding by table)."""
@@ -54,6 +62,30 @@ def test_sums_with_the_residual(dtype, m, width, alpha, fmt):
     x, delta = rows(m, m, width, dt), rows(m + 1, m, width, dt, 0.7)
     codes, scales = call(x, delta, alpha, width, rq.RQ_NORM_NONE, None, None, 0.0, fmt)
     h = x.double().cpu().numpy() + alpha * delta.double().cpu().numpy()
+    want, wscale = quantized(h, fmt)
+    assert np.array_equal(scales, wscale)
+    assert np.array_equal(codes, want), int((codes != want).sum())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", [rq.RQ_NORM_RMS, rq.RQ_NORM_LAYER], ids=["rms", "layer"])
+@pytest.mark.parametrize("m,width,parts", [(1500, 4096, "g"), (3000, 4096, "gb"), (700, 4096, ""), (300, 2560, "gb"), (1, 2048, "gb"),
+                                           (200, 8192, "gb"), (100, 16384, "g")])
+def test_normed_rows(m, width, parts, kind, fmt):
+    g = np.random.default_rng(m + width)
+    half = g.integers(1, 9, (m, width // 2)) * g.choice([-1, 1], (m, width // 2))
+    x = np.concatenate([half, -half], 1)
+    x[:, width // 4] *= 20
+    x[:, width // 4 + width // 2] *= 20
+    for row in x:
+        g.shuffle(row)
+    x = x.astype(np.float64)
+    assert (x ** 2).sum(1).max() < 2 ** 24 and not x.sum(1).any()
+    gamma = (1 + 0.2 * g.standard_normal(width)).astype(np.float32) if "g" in parts else None
+    beta = (0.1 * g.standard_normal(width)).astype(np.float32) if "b" in parts else None
+    d = [None if v is None else torch.from_numpy(v).cuda() for v in (gamma, beta)]
+    codes, scales = call(torch.from_numpy(x).half().cuda(), None, 0.0, width, kind, *d, EPS, fmt)
+    h = nt.normed(x, kind, None if gamma is None else gamma.astype(float), None if beta is None else beta.astype(float), EPS)
     want, wscale = quantized(h, fmt)
     assert np.array_equal(scales, wscale)
     assert np.array_equal(codes, want), int((codes != want).sum())
