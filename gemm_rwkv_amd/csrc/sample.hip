@@ -8,7 +8,7 @@
 // whose cumulative mass exceeds u times the kept mass.
 //
 // A token changes when an error moves any border between kept tokens over u's
-// place, and there may be 65536 of them, so weights are fp64 to 2^-47 and sums
+// place, and there may be 65536 of them, so weights are fp64 to 2^-46 and sums
 // fp64 in a fixed order: that, some 20 fp64 operations a logit, and the row's way
 // through one compute unit are what bounds the draw.
 //
@@ -58,8 +58,9 @@ __device__ __forceinline__ double horner(double p, double r, double c) {
   return p;
 }
 
-// 2^(d rate), above 2^-1022, to 2^-47 of its value, by Taylor's series in the part
-// of d rate past the nearest whole number.
+// 2^(d rate), above 2^-1022, by Taylor's series in the part r of d rate past the
+// nearest whole number.  The first term left out is 2^-46.7 of the value at r = -1/2,
+// beside some 2^-52 of rounding.
 __device__ __forceinline__ double pow2(double d, double rate) {
   constexpr double kRound = 0x1.8p52;  // with it added, the whole number is in the low bits
   const double a = __builtin_fma(d, rate, kRound), r = __builtin_fma(d, rate, -(a - kRound));

@@ -564,10 +564,14 @@ int rq_gemm_fp8_block(const uint8_t *xq, const uint8_t *sx, int64_t m, const rq_
  * or less (or NaN) takes the first of the largest logits, with logprob 0.
  * A NaN logit counts as -inf, NaN in top_p or min_p as no filter, in u as 0; -inf
  * is never drawn; beside +inf nothing else is.  A row with nothing to draw
- * gets token -1 and logprob -inf.  Weights and sums are fp64; a weight below
- * 2^-990 counts as 0.  top_p's border alone goes by weights rounded to whole
- * multiples of 2^-s, s = 62 less the bits of vocab but at most 51 (45 for 65536),
- * so that their sums are the same in any order.
+ * gets token -1 and logprob -inf.
+ * Weights and sums are fp64, weights to some 2^-46 of their value (2^-43 below
+ * 2^-100); one below 2^-990 counts as 0.  top_p's border alone goes by weights
+ * rounded to whole multiples of 2^-s, s = 62 less the bits of vocab but at most 51
+ * (45 for 65536), so that their sums are the same in any order.  A row's sums do
+ * not depend on the rows beside it, but they are made in one order up to 256
+ * rows and in another past that, which may move the last bits of logprob, and the
+ * token where u lies that close to a border.
  * rows < 2^21, vocab <= 2^20. */
 int rq_sample(int dtype, const void *logits, int64_t rows, int64_t vocab, int64_t ld, const float *temperature,
               const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,

@@ -74,3 +74,16 @@ def test_close_and_far_logits(dtype):
     u = list(g.random(rows))
     for kw in ({}, {"k": 77}, {"p": 0.37}, {"k": 3000, "p": 0.5}, {"T": 500.0, "p": 0.9}, {"k": 20000, "T": math.inf}):
         check_some(z, vocab, u=u, **kw)
+
+
+@pytest.mark.parametrize("rows,fewer", [(256, (1, 2, 255)), (600, (257, 300))])
+def test_bits_go_by_the_launch_shape(rows, fewer):
+    """Up to 256 rows, and past 256, a row's token and the bits of its probability are the same whatever the rows beside it."""
+    vocab = 20011
+    z = logits_of(12, rows, vocab, "f16")
+    u = list(np.random.default_rng(4).random(rows))
+    for kw in ({}, {"p": 0.8}, {"k": 40}, {"k": 3000, "m": 0.001}):
+        token, lp = run(z, vocab, u=u, **kw)
+        for n in fewer:
+            t, l = run(z[-n:], vocab, u=u[-n:], **kw)
+            assert np.array_equal(t, token[-n:]) and np.array_equal(l, lp[-n:])
