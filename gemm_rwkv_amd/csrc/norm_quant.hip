@@ -16,13 +16,13 @@
 // one is reduced.  A block of 128 columns is 16 consecutive lanes, so its
 // scale takes four lane moves and no barrier.
 //
-// h is made in fp64, of an x' in fp64 (exact unless x and alpha delta lie 2^18
-// apart) and of sums in fp64 over the threads' fp32 ones, which take x' in fp32:
-// with an x' or an h in fp32 some h in a million came out on the other side of a
-// border between two codes.
+// All of it is fp64, from x' (exact unless x and alpha delta lie 2^18 apart) over
+// the sums to h: with any of them in fp32 some h in a million came out on the
+// other side of a border between two codes.  A vector instruction in fp64 takes
+// no longer than one in fp32 here; what it costs is registers and conversions.
 //
-// 8192 rows of 4096 with residual, layer norm and block scales take 53 us, 4.5
-// TB/s, where a large copy reaches 5.0 (with x' in fp32 52, with h too 47).  A few rows take the
+// 8192 rows of 4096 with residual, layer norm and block scales take 54 us, 4.3
+// TB/s, where a large copy reaches 5.0 (x' and the sums in fp32 52, h too 47).  A few rows take the
 // latency of their reads and of two reductions: 2.8 us for one of 2048.
 #include "mix.h"
 #include "next_token.h"
@@ -103,8 +103,7 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
 constexpr uint32_t kNaN = 0x7fc00000u;
 constexpr uint32_t kPastFloat = 0x47f00000u;  // upper half of 2^128: what fp32 cannot say is not finite
 
-// Sums past fp32 (and NaN) make a row not finite: what overflows there must not
-// pass for a large norm.
+// Sums past fp32 (and NaN) make a row not finite.
 __device__ __forceinline__ bool past_float(double sum) { return !(__builtin_fabs(sum) <= 3.4028234663852886e38); }
 
 template <typename T, int NORM, int FMT, int NV>
@@ -148,16 +147,16 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
   int buf = 0;
   for (int row = begin; row < end; ++row, buf ^= 1) {
     double x[NV][8];
-    float xf[NV][8];  // for the statistics and x_out
     double h[FMT == ROW_BLOCK ? 1 : NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      up2<T>(xr[j].x, xf[j]);
-      up2<T>(xr[j].y, xf[j] + 2);
-      up2<T>(xr[j].z, xf[j] + 4);
-      up2<T>(xr[j].w, xf[j] + 6);
+      float f[8];
+      up2<T>(xr[j].x, f);
+      up2<T>(xr[j].y, f + 2);
+      up2<T>(xr[j].z, f + 4);
+      up2<T>(xr[j].w, f + 6);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = xf[j][i];
+      for (int i = 0; i < 8; ++i) x[j][i] = f[i];
       if (p.delta) {
         float d[8];
         up2<T>(dr[j].x, d);
@@ -167,36 +166,43 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[j][i] = __builtin_fma((double)p.alpha, (double)d[i], x[j][i]);
-          xf[j][i] = (float)x[j][i];
+          f[i] = (float)x[j][i];
         }
       }
-      if (p.x_out && on[j]) store8<T>(p.x_out, (size_t)row * p.ld + 8 * (j * blockDim.x + tid), xf[j]);
+      if (p.x_out && on[j]) store8<T>(p.x_out, (size_t)row * p.ld + 8 * (j * blockDim.x + tid), f);
     }
     if (row + 1 < end) fetch(row + 1);
 
     // statistics: two passes over the registers, sums in a fixed order
-    double mean = 0, rstd = 1;
+    double rstd = 1;
     if constexpr (NORM == NORM_LAYER) {
-      float s = 0.f;
+      double s = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (on[j])
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s += xf[j][i];
+          for (int i = 0; i < 8; ++i) s += x[j][i];
       const double w = sum64(s);
       if ((tid & 63) == 0) sums[buf][0][wave] = w;
       __syncthreads();
-      for (int w = 0; w < waves; ++w) mean += sums[buf][0][w];
-      mean = past_float(mean) ? __builtin_nan("") : mean * part;
+      double sum = 0;
+      for (int w = 0; w < waves; ++w) sum += sums[buf][0][w];
+      // the quotient, rounded right: a row of one value has no other mean
+      double mean = sum * part;
+      mean = __builtin_fma(__builtin_fma(-mean, (double)p.width, sum), part, mean);
+      if (past_float(sum)) mean = __builtin_nan("");
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] -= mean;
     }
     if constexpr (NORM != NORM_NONE) {
-      float s = 0.f;
-      const float m = (float)mean;
+      double s = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (on[j])
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s = __builtin_fmaf(xf[j][i] - m, xf[j][i] - m, s);
+          for (int i = 0; i < 8; ++i) s = __builtin_fma(x[j][i], x[j][i], s);
       const double w = sum64(s);
       if ((tid & 63) == 0) sums[buf][1][wave] = w;
       __syncthreads();
@@ -204,7 +210,6 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
       for (int w = 0; w < waves; ++w) ss += sums[buf][1][w];
       rstd = past_float(ss) ? __builtin_nan("") : inverse_root(__builtin_fma(ss, part, (double)p.eps));
     }
-    const double shift = -mean * rstd;
     // h, and the largest |h| as a bit pattern (NaN and infinities come out on top)
     uint64_t all = 0;
     uint8_t* codes = (uint8_t*)p.codes + (size_t)row * p.width;
@@ -218,8 +223,7 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         double n = x[j][i];
-        if constexpr (NORM == NORM_LAYER) n = __builtin_fma(n, rstd, shift);
-        if constexpr (NORM == NORM_RMS) n *= rstd;
+        if constexpr (NORM != NORM_NONE) n *= rstd;
         hj[i] = __builtin_fma(n, gm[KEEP ? j : 0][i], bt[KEEP ? j : 0][i]);
         if (!kBlocks && on[j]) all = max(all, __builtin_bit_cast(uint64_t, hj[i]) & ~0ull >> 1);
       }

@@ -508,11 +508,10 @@ int rq_head_gate_backward(int dtype, const void *y, const void *r, const void *k
  *     x' = x + alpha delta                          (delta NULL: x' = x)
  *     h  = n(x') gamma + beta                       (gamma NULL: ones, beta NULL: zeros)
  * with n(x') = x' (RQ_NORM_NONE), x' / sqrt(mean x'^2 + eps) (RQ_NORM_RMS) or
- * (x' - mean) / sqrt(var + eps) (RQ_NORM_LAYER).  x' and h are fp64, never rounded
- * to fewer bits before their codes are; the sums take x' in fp32, up to 32 of
- * a row's values added in fp32 and those sums in fp64, in an order that goes by
- * width alone.  x_out (may be NULL, may be x) gets x', by way of fp32, in `dtype`
- * (RQ_F16 or RQ_BF16, RQ_ERR_FORMAT otherwise).
+ * (x' - mean) / sqrt(var + eps) (RQ_NORM_LAYER).  x', the sums and h are fp64, never
+ * rounded to fewer bits before the codes are; the sums' order goes by width alone.
+ * x_out (may be NULL, may be x) gets x', by way of fp32, in `dtype` (RQ_F16 or
+ * RQ_BF16, RQ_ERR_FORMAT otherwise).
  * x, delta, x_out: [rows][ld], ld % 8 == 0; codes: [rows][width] bytes.
  * format says which codes and scales:
  *   RQ_FP8_E4M3_CH, RQ_I8_CH (width % 16 == 0): scales fp32 [rows] =

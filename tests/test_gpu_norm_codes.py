@@ -1,12 +1,10 @@
 """Codes of rq_norm_quantize that are those of the 64-bit h, byte for byte.
 
 x' = x + alpha delta has at most 35 bits (24 of alpha, 11 of a value, their lowest
-places less than 2^18 apart), so fp64 holds it.  With a norm the rows are of whole
-numbers, in pairs of opposite signs for the layer norm, whose sums and sums of
-squares stay below 2^24: fp32 sums of them are exact, and what is left is the error
-of 1 / sqrt and of the products in fp64, 2^-40 of h.  An h in fp32 is off by some
-2^-24 of itself; a border between two e4m3 codes lies within that of one h in 2^20
-or so, so of some millions of values several would get another code.
+places less than 2^18 apart), so fp64 holds it.  The sums and h are fp64 as well: an
+h is off by some 2^-42 of itself, and a border between two codes lies within that of
+one h in 2^38.  With a sum or an h in fp32 (2^-24) that is one in 2^20, and of some
+millions of values several would get another code: the rows are that many.
 """
 
 import numpy as np
@@ -89,3 +87,43 @@ def test_normed_rows(m, width, parts, kind, fmt):
     want, wscale = quantized(h, fmt)
     assert np.array_equal(scales, wscale)
     assert np.array_equal(codes, want), int((codes != want).sum())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", [rq.RQ_NORM_RMS, rq.RQ_NORM_LAYER], ids=["rms", "layer"])
+@pytest.mark.parametrize("dtype,m,width,alpha,mean", [("f16", 1700, 4096, 0.3, 0.0), ("bf16", 1500, 2560, None, 4.0), ("f16", 700, 8192, 1.0, 300.0),
+                                                      ("bf16", 200, 16384, -0.7, 0.5), ("f16", 5000, 272, 0.5, 1.0), ("bf16", 3000, 640, None, 0.0)])
+def test_any_rows(dtype, m, width, alpha, mean, kind, fmt):
+    if fmt == rq.RQ_FP8_E4M3_B128 and width % 128:
+        width = 256
+    dt, g = TYPES[dtype][0], np.random.default_rng(m)
+    x = rows(m, m, width, dt) + mean
+    delta = None if alpha is None else rows(m + 1, m, width, dt, 0.6)
+    alpha = 0.0 if alpha is None else float(np.float32(alpha))
+    gamma = (1 + 0.2 * g.standard_normal(width)).astype(np.float32)
+    beta = (0.1 * g.standard_normal(width)).astype(np.float32) if kind == rq.RQ_NORM_LAYER else None
+    d = [None if v is None else torch.from_numpy(v).cuda() for v in (gamma, beta)]
+    codes, scales = call(x, delta, alpha, width, kind, *d, EPS, fmt)
+    full = x.double().cpu().numpy()
+    if delta is not None:
+        full = full + alpha * delta.double().cpu().numpy()
+    h = nt.normed(full, kind, gamma.astype(float), None if beta is None else beta.astype(float), EPS)
+    want, wscale = quantized(h, fmt)
+    assert np.array_equal(scales, wscale), int((scales != wscale).sum())
+    assert np.array_equal(codes, want), int((codes != want).sum())
+
+
+@pytest.mark.parametrize("width", [640, 4096, 6016])
+@pytest.mark.parametrize("with_beta", [False, True])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_of_one_value(fmt, with_beta, width):
+    """Their variance is 0 and h is beta alone, exactly; without one the scales and codes are those of zeros."""
+    g = np.random.default_rng(3)
+    x = torch.from_numpy(np.repeat(g.standard_normal((20, 1)) * 10, width, 1)).half().cuda()
+    beta = (0.1 * g.standard_normal(width)).astype(np.float32)
+    codes, scales = call(x, None, 0.0, width, rq.RQ_NORM_LAYER, None, torch.from_numpy(beta).cuda() if with_beta else None, EPS, fmt)
+    if with_beta:
+        want, wscale = nt.quantize_rows(beta[None].astype(float).repeat(20, 0), fmt)
+        assert np.array_equal(codes, want) and np.array_equal(scales, wscale)
+    else:
+        assert not (codes & 127).any() and not scales.any()
