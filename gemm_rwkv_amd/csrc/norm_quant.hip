@@ -18,12 +18,14 @@
 //
 // All of it is fp64, from x' (exact unless x and alpha delta lie 2^18 apart) over
 // the sums to h: with any of them in fp32 some h in a million came out on the
-// other side of a border between two codes.  A vector instruction in fp64 takes
-// no longer than one in fp32 here; what it costs is registers and conversions.
+// other side of a border between two codes.
 //
 // 8192 rows of 4096 with residual, layer norm and block scales take 54 us, 4.3
-// TB/s, where a large copy reaches 5.0 (x' and the sums in fp32 52, h too 47).  A few rows take the
-// latency of their reads and of two reductions: 2.8 us for one of 2048.
+// TB/s, where a large copy reaches 5.0 (x' and the sums in fp32 52, h too 47), and
+// without residual 41, for 20 at the copy's rate: vector instructions then, some 36
+// a value.  One scale a row, whose quotients are in fp64, takes 73, and 61 to 63.  A
+// few rows take the latency of their reads and of two reductions: 2.8 us for one of
+// 2048.
 #include "mix.h"
 #include "next_token.h"
 
@@ -225,7 +227,8 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
         double n = x[j][i];
         if constexpr (NORM != NORM_NONE) n *= rstd;
         hj[i] = __builtin_fma(n, gm[KEEP ? j : 0][i], bt[KEEP ? j : 0][i]);
-        if (!kBlocks && on[j]) all = max(all, __builtin_bit_cast(uint64_t, hj[i]) & ~0ull >> 1);
+        // (both of one type: of two, max() would be that of doubles)
+        if (!kBlocks && on[j]) all = max(all, __builtin_bit_cast(uint64_t, __builtin_fabs(hj[i])));
       }
       if constexpr (FMT == ROW_BLOCK) {
         uint32_t u[8], t = 0;
@@ -288,6 +291,17 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
   }
 }
 
+// As few vectors a thread as 512 threads allow, and a row a workgroup until 4096
+// rows, then one more for each 4096.  In us, fp16 with residual:
+//   one vector or two, block scales: 1 x 4096 3.5 and 4.0, 1021 x 2048 6.0 and 6.2,
+//     1021 x 4096 10.2 and 10.6, 8192 x 2048 28.7 and 29.5; for more values two would
+//     do better, 8192 x 4096 55.5 and 51.7 (61 and 52 with one scale a row), at
+//     twice the registers for every row that is shorter;
+//   two or four: 1 x 8192 4.5 and 5.4, 1021 x 8192 19.0 and 17.7, 4096 x 8192 60
+//     and 61 (75 and 68);
+//   one, two, three, four and eight rows, block scales: 4000 x 4096 30 29 30 28 28,
+//     8192 x 4096 54 55 54 53 52, 16384 x 4096 108 102 100 98 97, 8192 x 8192 131 110
+//     111 108 107, 40000 x 1024 (ten by the rule) 71 61 59 60 61.
 template <typename T, int NORM, int FMT>
 hipError_t launch_format(const NormQuant& p, hipStream_t st) {
   const int vecs = p.width / 8;

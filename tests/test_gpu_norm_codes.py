@@ -127,3 +127,24 @@ def test_rows_of_one_value(fmt, with_beta, width):
         assert np.array_equal(codes, want) and np.array_equal(scales, wscale)
     else:
         assert not (codes & 127).any() and not scales.any()
+
+
+@pytest.mark.parametrize("fmt,most", [(rq.RQ_FP8_E4M3_CH, 448.0), (rq.RQ_I8_CH, 127.0)])
+def test_scale_of_the_largest_in_all_its_bits(fmt, most):
+    """Rows whose largest |h|, its bits rounded to 53 of 64 as a double of them would be, gives another scale in fp32."""
+    alpha, g = float(np.float32(0.1)), np.random.default_rng(5)
+    gamma = (1 + 0.2 * g.standard_normal(16)).astype(np.float32)
+    v = (1024 + np.arange(1024)) / 1024.0
+    found = []
+    for j in range(16):
+        h = (v[:, None] + alpha * v) * float(gamma[j])
+        rounded = h.view(np.uint64).astype(np.float64).astype(np.uint64).view(np.float64)
+        found += [(j, v[a], v[b]) for a, b in np.argwhere((h / most).astype(np.float32) != (rounded / most).astype(np.float32))]
+    assert len(found) >= 4
+    x, delta = np.zeros((2, len(found), 16))
+    for r, (j, a, b) in enumerate(found):
+        x[r, j], delta[r, j] = a, b
+    h = (x + alpha * delta) * gamma.astype(float)
+    _, scales = call(torch.from_numpy(x).half().cuda(), torch.from_numpy(delta).half().cuda(), alpha, 16, rq.RQ_NORM_NONE,
+                     torch.from_numpy(gamma).cuda(), None, 0.0, fmt)
+    assert np.array_equal(scales, (h.max(1) / most).astype(np.float32))
