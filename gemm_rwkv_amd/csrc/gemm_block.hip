@@ -16,13 +16,15 @@
 // codes counting as 2^-6 (measured: 448 + 2^-5 * 0.9 is 448, and nothing is lost
 // across groups of eight or beside the accumulator).  A y is off by up to 7 * 2^-13
 // of each group's largest product: some 2^-14 of y on ordinary rows, far more of a
-// y in which large products cancel.  A y in fp32 is due more, and up to 16 rows
-// more costs nothing, as the weight's way from HBM is the bound (16 x 65536 x 4096
-// in fp16 53.0 us, and 53.2; 1 x 2048 x 2048 2.9 and 3.2).  There the codes are
-// widened to fp16, which holds each of them, their products go through the fp16
+// y in which large products cancel.  A y in fp32 is due more, and up to 16 rows,
+// where the weight's way from HBM is the bound, more costs little.  There the codes
+// are widened to fp16, which holds each of them, their products go through the fp16
 // instruction, which keeps fp32, and each block's sum is scaled as it joins the
-// row's.  With more rows the matrix instructions count, and a 16-bit y takes the
-// fp8 one (64 x 4096 x 4096 7.4 us, widened 8.9; 1024 x 16384 x 4096 62 and 155).
+// row's.  In us, fp8 instruction and widened: 1 x 2048 x 2048 2.9 and 3.2, 1 x 16384 x
+// 4096 13.3 and 13.8, 16 x 65536 x 4096 53.0 and 53.5.  With more rows the matrix
+// instructions count, and a 16-bit y takes the fp8 one: 32 x 2048 x 2048 3.5 and
+// 4.5, 32 x 16384 x 4096 13.1 and 14.1, 64 x 4096 x 4096 7.4 and 9.1, 1024 x 16384 x
+// 4096 62 and 149.
 //
 // Up to some 64 rows the weight's way from HBM bounds it: 32 x 65536 x 4096 into
 // fp32 takes 63 us, 4.4 TB/s.  Past that it is the copies from L2 to LDS, which a
@@ -359,8 +361,10 @@ hipError_t launch_tile(const BlockGemm& p, hipStream_t st) {
 
 // The largest tile that still gives most of the 256 compute units one.  Measured
 // in us on both sides of each border (m x n x k, 16-bit y):
-//   16 x 16, waves 8, or 16 x 32, waves 4, for up to 16 rows: 16 x 16384 x 4096
-//     15.9 and 16.0, 16 x 65536 x 4096 44.6 and 41.6, 16 x 2048 x 2048 3.5 and 3.9;
+//   16 x 16, waves 8, or 16 x 32, waves 4, for up to 16 rows: 16 x 2048 x 2048 3.9
+//     and 4.6, 16 x 16384 x 4096 17.5 and 17.1, 16 x 32768 x 4096 30.6 and 28.8, 16 x
+//     65536 x 4096 56.9 and 53.9; 1 x 16384 x 4096 15.7 and 17.4, 1 x 65536 x 4096
+//     49.5 and 51.7, 1 x 65536 x 2048 31 and 25;
 //   32 x 16 or 32 x 32: 64 x 2048 x 2048 (256 or 128 tiles) 4.2 and 4.6, 64 x 4096
 //     x 4096 (512 or 256) 9.8 and 8.6;
 //   32 x 32 or 32 x 64: 64 x 4096 x 4096 (256 or 128) 8.6 and 10.6, 128 x 4096 x
@@ -377,8 +381,9 @@ hipError_t launch_tile(const BlockGemm& p, hipStream_t st) {
 // A y in fp32 does twice the matrix work, and past 64 x 64 it always takes 128 x
 // 128 in two stages: 512 x 4096 x 4096 (128 tiles) 46, in tiles of 64 x 64 32, 200
 // x 10240 x 2560 (160) 31.5 and 33, 1000 x 16384 x 4096 150 (four stages 183).
-// Scales of a k so long that they do not fit LDS beside the stages go with the
-// 128 x 128 tile too, which takes four blocks' at a time.
+// Scales of a k so long that they do not fit LDS beside the stages (past 64512, or
+// 739840 for up to 16 rows) go with the 128 x 128 tile too, which takes four blocks'
+// at a time: 2 x 200 x 65664 280 us, in tiles of 16 x 16 23.5.
 template <int OUT>
 hipError_t launch_out(const BlockGemm& p, hipStream_t st) {
   constexpr bool F32OUT = OUT == OUT_F32;

@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(512) norm_quant_kernel(NormQuant p, int run) {
 // As few vectors a thread as 512 threads allow, and a row a workgroup until 4096
 // rows, then one more for each 4096.  In us, fp16 with residual:
 //   one vector or two, block scales: 1 x 4096 3.5 and 4.0, 1021 x 2048 6.0 and 6.2,
-//     1021 x 4096 10.2 and 10.6, 8192 x 2048 28.7 and 29.5; for more values two would
-//     do better, 8192 x 4096 55.5 and 51.7 (61 and 52 with one scale a row), at
-//     twice the registers for every row that is shorter;
+//     1021 x 4096 10.2 and 10.6, 8192 x 2048 28.7 and 29.5; many rows of some 4096
+//     would rather have two, 8192 x 4096 55.5 and 51.7 (61 and 52 with one scale a
+//     row);
 //   two or four: 1 x 8192 4.5 and 5.4, 1021 x 8192 19.0 and 17.7, 4096 x 8192 60
 //     and 61 (75 and 68);
 //   one, two, three, four and eight rows, block scales: 4000 x 4096 30 29 30 28 28,

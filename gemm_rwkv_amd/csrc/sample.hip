@@ -29,11 +29,15 @@
 // 64 bits), so the order of the atomic adds changes no bit.
 //
 // A workgroup has a row; its waves own consecutive parts of it, 8 logits a lane
-// and turn.  One row of 65536 in fp16 (128 KB) takes 15.7 us with top_k 50, top_p
-// and min_p (4 for the largest, 5 for the list, 5 to rank and draw), 21.4 with no
-// filter (13 for the weights' sums, 3 to find the place), 40.6 with top_p alone
-// (20 for the histogram, 7 to fetch the border's class, then the draw); 509 rows
-// of 50277 in bf16 take 41.4 with no filter, 1.2 TB/s: fp64 operations, not bytes.
+// and turn.  One row of 65536 in fp16 (128 KB) takes 15.9 us with top_k 50, top_p
+// and min_p (4 for the largest, 5 for the list, 5 to rank and draw), 21.6 with no
+// filter (13 for the weights' sums, 3 to find the place), 41 with top_p alone
+// (20 for the histogram, 7 to fetch the border's class, then the draw), 44 with
+// top_k 5000.  509 rows of 50277 in bf16 take 41 with no filter, 1.2 TB/s, of which
+// the weights' instructions are some 13; the rest is the pass for the largest
+// logit before them, and two workgroups to a compute unit that take the same
+// passes at the same time.  509 rows of 65536 in fp16 take 123 with top_p alone:
+// the draw's walk makes a weight of every logit, also of those past the cut.
 #include "mix.h"
 #include "next_token.h"
 
@@ -946,10 +950,11 @@ template <typename T>
 hipError_t launch_type(const Sample& p, hipStream_t st) {
   // Up to a row for each of 256 compute units, the row's own time counts: 16 waves.
   // Past that two workgroups of 8 overlap on a unit (one's reads and barriers with
-  // the other's arithmetic).  Rows of 65536 in fp16, in us with 8 and 16 waves: 300
-  // rows 42 and 47 with no filter, 27 and 35 with top_k 50, 109 and 95 with top_p
-  // alone, 95 and 74 with a mixture; 509 rows 46 and 51, 31 and 38, 122 and 127, 99
-  // and 94; 900 rows 81 and 96, 53 and 72, 190 and 206, 133 and 145.
+  // the other's arithmetic).  Rows of 65536 in fp16, in us with 8 and 16 waves: 256
+  // rows 30 and 28 with no filter, 24 and 23 with top_k 50, 95 and 69 with top_p
+  // alone, 79 and 64 with a mixture; 300 rows 42 and 47, 27 and 36, 109 and 95, 95
+  // and 75; 509 rows 47 and 51, 31 and 39, 122 and 127, 98 and 94; 900 rows 80 and
+  // 96, 53 and 74, 187 and 207, 133 and 146.
   if (p.rows > 256)
     hipLaunchKernelGGL((sample_kernel<T, 512>), dim3(p.rows), dim3(512), 0, st, p);
   else

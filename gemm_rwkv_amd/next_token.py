@@ -36,7 +36,8 @@ def _served(*ts):
 def norm_quantize(x, delta=None, gamma=None, beta=None, norm="layer", eps=NORM_EPS, fmt=rq.RQ_FP8_E4M3_B128):
     """(x + delta, codes uint8 [rows][width], scales) of the norm ("layer",
     "rms" or None) of x + delta.  Scales are uint8 [rows][block_scale_row(width)]
-    in rq.RQ_FP8_E4M3_B128, fp32 [rows] in rq.RQ_FP8_E4M3_CH and rq.RQ_I8_CH."""
+    in rq.RQ_FP8_E4M3_B128, fp32 [rows] in rq.RQ_FP8_E4M3_CH and rq.RQ_I8_CH.
+    (rq.rq_norm_quantize also takes a factor of delta, and writes the sum in place.)"""
     _rows(x=x, delta=delta)
     (m, c) = x.shape
     if norm not in NORMS:
@@ -98,7 +99,11 @@ def sample(logits, temperature=None, top_k=None, top_p=None, min_p=None, u=None,
     of logits [rows][vocab] in fp16, bf16 or fp32.  The filters (rq.h,
     rq_sample) and u, the uniform numbers in [0, 1) that decide, are numbers or
     tensors with one value a row (top_k int32, the others fp32); without u it is
-    drawn from `generator`.  A row with nothing to draw gets token -1."""
+    drawn from `generator`.  A row with nothing to draw gets token -1.
+
+    A number is written to a tensor by a launch of its own, some 4 us of each
+    call, and so is u: one row of 65536 by three filters takes 15.5 us a call with
+    tensors, 26 with numbers, 31 with u drawn as well.  Loops keep tensors."""
     if logits.dtype not in _CODE_Y:
         raise TypeError("logits is %s, not float16, bfloat16 or float32" % logits.dtype)
     if logits.dim() != 2 or logits.shape[1] == 0:
@@ -184,7 +189,9 @@ def main(argv=None):
     layer, head = TimeMix(args.width).quantize(), Head(args.width, args.vocab).quantize()
     gen = torch.Generator("cuda").manual_seed(args.seed)
     embed = torch.randn(args.vocab, args.width, device="cuda", generator=gen).half()
-    how = dict(temperature=args.temperature, top_k=args.top_k, top_p=args.top_p, min_p=args.min_p, generator=gen)
+    how = {q: torch.full((n,), v, device="cuda") for q, v in
+           (("temperature", args.temperature), ("top_p", args.top_p), ("min_p", args.min_p))}
+    how.update(top_k=torch.full((n,), args.top_k, dtype=torch.int32, device="cuda"), generator=gen)
     shift, state = layer.states(n)
     slots = torch.arange(n, dtype=torch.int32, device="cuda")
     cu, one = offsets(lens), offsets([1] * n)

@@ -4,11 +4,11 @@ oracle.
 Whole numbers first: codes of -2..2 and scales of 1/2, 1 and 2 make every
 product and sum exact in any order, so y has to be the rounded exact value.
 Then codes of all sizes.  A y in fp32 comes from fp32 sums of exact products:
-k * 2^-24 of sum |x w| bounds any order of k additions.  A 16-bit y comes
-from the fp8 instruction, which cuts products 13 places below the largest
-exponent among them, so that each of the 128 products of a block loses less
-than 2^-13 of the block's largest one, and is rounded by half a step (2^-11,
-2^-8) of y.
+k * 2^-24 of sum |x w| bounds any order of k additions.  A 16-bit y is rounded
+by half a step (2^-11, 2^-8) and, of more than 16 rows, comes from the fp8
+instruction, which cuts each eight products 13 places below the largest exponent
+among them: here 2^-13 of the block's largest product is allowed for each of the
+128 (test_gpu_gemm_block_sums goes by the eights).
 """
 
 import numpy as np

@@ -5,9 +5,9 @@ graph.
 
 Each stage is held to the oracle of what the one before it left: the logits to
 the product of the codes (k * 2^-24 of sum |x w|, fp32 sums of exact products),
-the tokens to the draw from the logits (equal), the codes to the norm.  An h
-computed in fp32 is off by less than 2^-17 of S = |n gamma| + |gamma| mean|x| /
-rms + |beta|; a code's value by half a step more, 2^-4 of h or 2^-10 of the scale.
+the tokens to the draw from the logits (equal), the codes to the norm, to within
+what an h in fp32 would need (the kernel's is fp64): 2^-17 of S = |n gamma| + |gamma|
+mean|x| / rms + |beta|; a code's value half a step more, 2^-4 of h or 2^-10 of the scale.
 """
 
 import numpy as np

@@ -1,11 +1,12 @@
 """rq_norm_quantize on the GPU against the 64-bit oracle.
 
 Where h is the input itself (no norm, no residual, no parameters) codes and
-scales are the oracle's byte for byte.  Elsewhere h is computed in fp32: its sums
-have at most 64 sequential terms per thread and 8 per workgroup, its roots and
-quotients one rounding each, so with S = |n gamma| + |gamma| mean|x| / rms + |beta|
-an h is off by less than 128 * 2^-24 S = 2^-17 S.  A code's value is off by half
-a step more: 2^-4 of h in e4m3 (2^-10 of the scale where it is subnormal), half
+scales are the oracle's byte for byte.  Elsewhere the bound here is what an h in
+fp32 would need: its sums have at most 64 sequential terms per thread and 8 per
+workgroup, its roots and quotients one rounding each, so with S = |n gamma| + |gamma|
+mean|x| / rms + |beta| such an h is off by less than 128 * 2^-24 S = 2^-17 S.  (The
+kernel's is fp64; test_gpu_norm_codes holds it to that.)  A code's value is off by
+half a step more: 2^-4 of h in e4m3 (2^-10 of the scale where it is subnormal), half
 the scale in int8.
 """
 

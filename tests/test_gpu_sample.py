@@ -1,6 +1,6 @@
 """rq_sample on the GPU against the 64-bit oracle: the tokens are equal, the
 log-probabilities within 1e-6 + 2^-23 of theirs (fp64 sums, one rounding to
-fp32; the weights are exact to 2^-47)."""
+fp32; the weights are exact to 2^-46)."""
 
 import math
 
