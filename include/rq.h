@@ -521,8 +521,9 @@ int rq_head_gate_backward(int dtype, const void *y, const void *r, const void *k
  *     ceil(width/512)], one power of two per 128 columns by the rule of the
  *     weight format, for rq_gemm_fp8_block.
  * A row (a block of 128 columns) that holds an h which is not finite gets a NaN
- * scale (0xff) and codes of zero, so that products of it are NaN; a sum or
- * sum of squares past fp32 counts as not finite.  width <= 16384 (RQ_ERR_SHAPE),
+ * scale (0xff) and codes of zero, so that products of it are NaN.  An h of 2^128
+ * or more, and a row's sum or sum of squares past fp32, count as not finite; an x'
+ * does not, and is infinite in x_out alone.  width <= 16384 (RQ_ERR_SHAPE),
  * eps >= 0 and norm one of the three (RQ_ERR_VALUE). */
 enum rq_norm { RQ_NORM_NONE = 0, RQ_NORM_RMS = 1, RQ_NORM_LAYER = 2 };
 int rq_norm_quantize(int dtype, int norm, const void *x, const void *delta, float alpha, int64_t rows, int64_t width,

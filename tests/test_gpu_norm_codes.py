@@ -148,3 +148,22 @@ def test_scale_of_the_largest_in_all_its_bits(fmt, most):
     _, scales = call(torch.from_numpy(x).half().cuda(), torch.from_numpy(delta).half().cuda(), alpha, 16, rq.RQ_NORM_NONE,
                      torch.from_numpy(gamma).cuda(), None, 0.0, fmt)
     assert np.array_equal(scales, (h.max(1) / most).astype(np.float32))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_sums_past_fp32(fmt):
+    """x' beyond fp32 is infinite in x_out, and counts for h where a gamma brings it back; an h beyond fp32 is not finite."""
+    width = 256
+    x, delta = torch.zeros(3, width).to("cuda", torch.bfloat16), rows(4, 3, width, torch.bfloat16, 0.02)
+    delta[1] = torch.linspace(-3e38, 3e38, width).to("cuda", torch.bfloat16)
+    x_out = torch.empty_like(x)
+    for gamma, finite in ((1e-4, True), (1.0, False)):
+        gv = torch.full((width,), gamma, device="cuda")
+        codes, scales = call(x, delta, 16.0, width, rq.RQ_NORM_NONE, gv, None, 0.0, fmt, x_out)
+        h = 16.0 * delta.double().cpu().numpy() * float(np.float32(gamma))
+        assert torch.isinf(x_out[1]).any() and not torch.isinf(x_out[[0, 2]]).any()
+        if not finite:
+            h[1] = np.where(np.abs(h[1]) >= 2.0 ** 128, np.inf, h[1])
+        want, wscale = nt.quantize_rows(h, fmt)
+        assert np.array_equal(scales, wscale, equal_nan=fmt != rq.RQ_FP8_E4M3_B128)
+        assert np.array_equal(codes, want)
